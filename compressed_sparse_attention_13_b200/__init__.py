@@ -10,7 +10,9 @@ Names follow the C ABI: ``csa_compress``, ``csa_quantize``, ``indexer_score``,
 ``topk_select``, ``sparse_mqa_attn``, ``hca_attn``, ``window_attn``, ``csa_decode``,
 ``csa_prefill``, ``csa_workspace_size``, ``csa_device_status``, and
 ``csa_decode_noalloc`` (csa_decode on the library's fixed device scratch, for
-callers that cannot allocate).
+callers that cannot allocate).  The grouped-head calls ``paged_append``,
+``paged_decode_attn``, ``prompt_attn`` and ``csa_gqa_workspace_size`` take a
+``GqaParams``.
 """
 from __future__ import annotations
 
@@ -21,9 +23,11 @@ from dataclasses import dataclass
 F32, BF16, FP8_S64, MXFP4 = 0, 1, 2, 3
 OP_SPARSE_ATTN, OP_HCA_ATTN, OP_DECODE, OP_PREFILL, OP_WINDOW_ATTN = 0, 1, 2, 3, 4
 OP_SHARD_SELECT, OP_SHARD_ATTEND, OP_HCA_SHARD = 5, 6, 7
+OP_PAGED_DECODE, OP_PROMPT_ATTN = 8, 9
 FLAG_BATCH_INVARIANT = 0x1
 FLAG_QI_BF16 = 0x2
 FLAG_INDEXER_FP8 = 0x4
+FLAG_ROT_PAIRS = 0x8
 DEV_BAD_INDEX, DEV_RANGE, DEV_TIMEOUT = 0x1, 0x2, 0x4
 NOALLOC_SCRATCH_BYTES = 32 << 20   # CSA_NOALLOC_SCRATCH_BYTES
 ERR_WORKSPACE = -4
@@ -53,10 +57,25 @@ def params(m, window, top_k, n_heads, head_dim, idx_heads, idx_dim, scale,
                   act_fmt, kv_fmt, idx_fmt, flags)
 
 
+class GqaParams(C.Structure):
+    """Mirror of ``csa_gqa_params``."""
+    _fields_ = [("n_heads", C.c_int32), ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("page_size", C.c_int32), ("window", C.c_int32), ("rot_dim", C.c_int32),
+                ("scale", C.c_float), ("act_fmt", C.c_int32), ("cache_fmt", C.c_int32),
+                ("flags", C.c_uint32)]
+
+
+def gqa_params(n_heads, n_kv_heads, head_dim, scale, page_size=16, window=0, rot_dim=0, act_fmt=BF16,
+               cache_fmt=BF16, flags=0) -> GqaParams:
+    return GqaParams(n_heads, n_kv_heads, head_dim, page_size, window, rot_dim, float(scale), act_fmt,
+                     cache_fmt, flags)
+
+
 EXPORTS = ["csa_compress", "csa_quantize", "indexer_score", "topk_select", "sparse_mqa_attn",
            "hca_attn", "window_attn", "csa_decode", "csa_prefill", "csa_workspace_size",
            "csa_device_status", "csa_strerror", "csa_version", "csa_decode_noalloc",
-           "csa_shard_select", "csa_shard_attend", "hca_shard_attend", "attn_merge"]
+           "csa_shard_select", "csa_shard_attend", "hca_shard_attend", "attn_merge", "paged_append",
+           "paged_decode_attn", "prompt_attn", "csa_gqa_workspace_size"]
 
 
 def lib():
@@ -89,6 +108,12 @@ def lib():
         L.attn_merge.argtypes = [PP, I32, I32, P, P, P, P, P]
         L.csa_workspace_size.restype = C.c_size_t
         L.csa_workspace_size.argtypes = [PP, I32, I32, I64, I64]
+        GP = C.POINTER(GqaParams)
+        L.paged_append.argtypes = [GP, I32, I64, P, P, P, I64, P, I64, P, I64, P, P, P, P, P, P, P, I64, P, I64, P]
+        L.paged_decode_attn.argtypes = [GP, I32, P, I64, P, P, P, P, I64, P, I64, P, P, P, P, C.c_size_t, P]
+        L.prompt_attn.argtypes = [GP, I32, P, I64, I64, P, I64, P, I64, I64, P, P, P, P, P, C.c_size_t, P]
+        L.csa_gqa_workspace_size.restype = C.c_size_t
+        L.csa_gqa_workspace_size.argtypes = [GP, I32, I32, I64, I64]
         L.csa_device_status.argtypes = [P, C.POINTER(C.c_uint32), I32]
         L.csa_strerror.restype = C.c_char_p
         L.csa_strerror.argtypes = [C.c_int]
@@ -273,3 +298,137 @@ def csa_device_status(reset: bool = True, stream=None) -> int:
     flags = C.c_uint32(0)
     _ok("csa_device_status", lib().csa_device_status(_s(stream), C.byref(flags), int(reset)))
     return flags.value
+
+
+# ------------------------------------------------- grouped-head attention
+def gqa_workspace_size(p: GqaParams, op: int, n_seq: int, n_tokens: int, n_ctx: int) -> int:
+    return lib().csa_gqa_workspace_size(C.byref(p), op, n_seq, n_tokens, n_ctx)
+
+
+def empty_paged(p: GqaParams, n_pages: int, device="cuda"):
+    """Allocate (with torch) the key and value pages of a paged cache: (k, v), each
+    [n_pages][n_kv_heads][page_size][head_dim] in p.cache_fmt."""
+    lead = (n_pages, p.n_kv_heads, p.page_size)
+    caches = []
+    for _ in range(2):
+        st = empty_stored(p.cache_fmt, n_pages * p.n_kv_heads * p.page_size, p.head_dim, device)
+        st.data = st.data.view(*lead, -1)
+        if st.scales is not None:
+            st.scales = st.scales.view(*lead, -1)
+        caches.append(st)
+    return tuple(caches)
+
+
+def _act_dtype(p):
+    import torch
+    return torch.float32 if p.act_fmt == F32 else torch.bfloat16
+
+
+def _rows_of(t, n, heads, p, name):
+    """(pointer, token stride in elements) of [n][heads][d] rows; the rows of one token are
+    dense, those of different tokens any stride apart."""
+    d = p.head_dim
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.dtype != _act_dtype(p):
+        raise ValueError(f"{name} must be {_act_dtype(p)}, got {t.dtype}")
+    if tuple(t.shape) != (n, heads, d):
+        raise ValueError(f"{name} must be [{n}][{heads}][{d}], got {list(t.shape)}")
+    s = t.stride()
+    if s[2] != 1 or (heads > 1 and s[1] != d):
+        raise ValueError(f"the heads of one token of {name} must be dense")
+    return t.data_ptr(), s[0] if n > 1 else heads * d
+
+
+def _dense(t, shape, dtype, name):
+    """Pointer of a dense tensor of this shape and type (None: no tensor)."""
+    if t is None:
+        return None
+    if tuple(t.shape) != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    return _p(t)
+
+
+def _caches(p, k_cache, v_cache, block_table, n_seq):
+    import torch
+    n_pages = k_cache.data.shape[0]
+    lead = (n_pages, p.n_kv_heads, p.page_size)
+    fp8 = p.cache_fmt == FP8_S64
+    dtype = {F32: torch.float32, BF16: torch.bfloat16}.get(p.cache_fmt, torch.uint8)
+    ptrs = []
+    for st, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if st.fmt != p.cache_fmt:
+            raise ValueError(f"{name} is stored in format {st.fmt}, the parameters name {p.cache_fmt}")
+        ptrs.append(_dense(st.data, lead + (p.head_dim,), dtype, name))
+        ptrs.append(_dense(st.scales, lead + (p.head_dim // 64,), torch.float32, name + " scales") if fp8 else None)
+    if block_table.dim() != 2 or block_table.shape[0] != n_seq:
+        raise ValueError(f"block_table must be [{n_seq}][max_pages], got {list(block_table.shape)}")
+    max_pages = block_table.shape[1]
+    table = _dense(block_table, (n_seq, max_pages), torch.int32, "block_table")
+    return (*ptrs, n_pages, table, max_pages)
+
+
+class _On:
+    """Makes the device of `t` current for a call (launches and the default
+    stream go by the current device) and refuses tensors of another one."""
+
+    def __init__(self, t, *others):
+        import torch
+        for o in others:
+            if o is not None and o.device != t.device:
+                raise ValueError(f"tensors on different devices: {t.device}, {o.device}")
+        self.guard = None if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *e):
+        if self.guard is not None:
+            self.guard.__exit__(*e)
+
+
+def paged_append(p: GqaParams, n_seq: int, n_tokens: int, cu_q, pos0, q, k, v, inv_freq, q_out, k_out,
+                 k_cache: Stored, v_cache: Stored, block_table, stream=None):
+    """q [n_tokens][H][d] (or None), k, v [n_tokens][HK][d]; cu_q int32 [n_seq + 1] or None
+    (one token per sequence); pos0 int64 [n_seq]; inv_freq float64 [rot_dim / 2] or None."""
+    import torch
+    H, HK, d, act = p.n_heads, p.n_kv_heads, p.head_dim, _act_dtype(p)
+    qp, ql = _rows_of(q, n_tokens, H, p, "q") if q is not None else (None, 0)
+    kp, kl = _rows_of(k, n_tokens, HK, p, "k")
+    vp, vl = _rows_of(v, n_tokens, HK, p, "v")
+    args = (_dense(cu_q, (n_seq + 1,), torch.int32, "cu_q"), _dense(pos0, (n_seq,), torch.int64, "pos0"), qp, ql, kp,
+            kl, vp, vl, _dense(inv_freq, (p.rot_dim // 2,), torch.float64, "inv_freq") if p.rot_dim > 0 else None,
+            _dense(q_out, (n_tokens, H, d), act, "q_out"), _dense(k_out, (n_tokens, HK, d), act, "k_out"),
+            *_caches(p, k_cache, v_cache, block_table, n_seq))
+    with _On(k, q, v, cu_q, pos0, inv_freq, q_out, k_out, k_cache.data, v_cache.data, block_table):
+        _ok("paged_append", lib().paged_append(C.byref(p), n_seq, n_tokens, *args, _s(stream)))
+
+
+def paged_decode_attn(p: GqaParams, batch: int, q, k_cache: Stored, v_cache: Stored, block_table, q_pos, sinks,
+                      out, workspace, stream=None):
+    """q, out [batch][H][d]; q_pos int64 [batch]; sinks float32 [H] or None."""
+    import torch
+    qp, ql = _rows_of(q, batch, p.n_heads, p, "q")
+    wp, wb = _ws(workspace)
+    args = (qp, ql, *_caches(p, k_cache, v_cache, block_table, batch), _dense(q_pos, (batch,), torch.int64, "q_pos"),
+            _dense(sinks, (p.n_heads,), torch.float32, "sinks"),
+            _dense(out, (batch, p.n_heads, p.head_dim), _act_dtype(p), "out"), wp, wb)
+    with _On(q, k_cache.data, v_cache.data, block_table, q_pos, sinks, out, workspace):
+        _ok("paged_decode_attn", lib().paged_decode_attn(C.byref(p), batch, *args, _s(stream)))
+
+
+def prompt_attn(p: GqaParams, n_seq: int, q, k, v, cu_q, cu_k, sinks, out, workspace, stream=None):
+    """q, out [n_q][H][d], k, v [n_k][HK][d]; cu_q, cu_k int32 [n_seq + 1]; sinks float32 [H]
+    or None."""
+    import torch
+    n_q, n_k = q.shape[0], k.shape[0]
+    qp, ql = _rows_of(q, n_q, p.n_heads, p, "q")
+    kp, kl = _rows_of(k, n_k, p.n_kv_heads, p, "k")
+    vp, vl = _rows_of(v, n_k, p.n_kv_heads, p, "v")
+    wp, wb = _ws(workspace)
+    args = (qp, ql, n_q, kp, kl, vp, vl, n_k, _dense(cu_q, (n_seq + 1,), torch.int32, "cu_q"),
+            _dense(cu_k, (n_seq + 1,), torch.int32, "cu_k"), _dense(sinks, (p.n_heads,), torch.float32, "sinks"),
+            _dense(out, (n_q, p.n_heads, p.head_dim), _act_dtype(p), "out"), wp, wb)
+    with _On(q, k, v, cu_q, cu_k, sinks, out, workspace):
+        _ok("prompt_attn", lib().prompt_attn(C.byref(p), n_seq, *args, _s(stream)))

@@ -4,6 +4,7 @@
 
 #include <mutex>
 
+#include "api_common.h"
 #include "kernels.h"
 
 namespace csa {
@@ -29,10 +30,6 @@ cudaError_t ensure_smem_impl(const void* kernel, size_t bytes) {
     return e;
 }
 
-static bool aligned16(const void* p) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-static bool act_ok(int f) { return f == CSA_F32 || f == CSA_BF16; }
-static bool kv_ok(int f) { return f == CSA_F32 || f == CSA_BF16 || f == CSA_FP8_S64; }
 static bool idx_ok(int f) { return f == CSA_F32 || f == CSA_BF16 || f == CSA_MXFP4; }
 
 static int check_params(const csa_params* p, bool need_idx, bool need_attn) {
@@ -49,12 +46,6 @@ static int check_params(const csa_params* p, bool need_idx, bool need_attn) {
         if (!idx_ok(p->idx_fmt) || p->top_k <= 0) return CSA_ERR_ARG;
     }
     return CSA_OK;
-}
-
-static int cuda_status(cudaError_t e) {
-    if (e == cudaSuccess) return CSA_OK;
-    if (e == cudaErrorInvalidValue) return CSA_ERR_UNSUPPORTED;
-    return CSA_ERR_CUDA;
 }
 
 // ------------------------------------------------------------ attention

@@ -101,4 +101,53 @@ cudaError_t launch_topk_merge(int64_t rows, int n_parts, int k, const float* can
                               int64_t entry0, int64_t n_entries, int32_t* sel_global, int32_t* sel_local,
                               int32_t* n_local, void* ws, int m, int W, cudaStream_t s);
 
+// ---------------------------------------------------- grouped-head attention
+struct PagedAppendArgs {
+    int H, HK, D, page_size, rot_dim, rot_pairs, act_fmt, cache_fmt;
+    int n_seq;
+    int64_t n_tokens;
+    const int32_t* cu_q;     // [n_seq + 1] or null: one token per sequence
+    const int64_t* pos0;     // [n_seq]
+    const void *q, *k, *v;   // q may be null
+    int64_t q_ld, k_ld, v_ld;
+    const double* inv_freq;  // [rot_dim / 2]
+    void *q_out, *k_out;     // k_out may be null
+    void *k_cache, *v_cache;
+    float *k_scales, *v_scales;
+    int64_t n_pages, max_pages;
+    const int32_t* block_table;  // [n_seq][max_pages]
+};
+cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s);
+
+struct PagedDecodeArgs {
+    int H, HK, D, page_size, W, act_fmt, cache_fmt, invariant;
+    float scale;
+    int64_t batch;
+    const void* q;  // [batch][H][D], rows q_ld apart
+    int64_t q_ld;
+    const void *k_cache, *v_cache;  // [n_pages][HK][page_size][D]
+    const float *k_scales, *v_scales;
+    int64_t n_pages, max_pages;
+    const int32_t* block_table;  // [batch][max_pages]
+    const int64_t* q_pos;        // [batch]
+    const float* sinks;          // [H] or null
+    void* out;                   // [batch][H][D]
+};
+cudaError_t launch_paged_decode_simt(const PagedDecodeArgs& a, cudaStream_t s);
+
+struct PromptArgs {
+    int H, HK, D, W, act_fmt, n_seq;
+    float scale;
+    const void *q, *k, *v;  // token rows q_ld, k_ld, v_ld apart
+    int64_t q_ld, k_ld, v_ld, n_q, n_k;
+    const int32_t *cu_q, *cu_k;  // [n_seq + 1]
+    const float* sinks;          // [H] or null
+    void* out;                   // [n_q][H][D]
+};
+cudaError_t launch_prompt_simt(const PromptArgs& a, cudaStream_t s);
+
+// The sequence of packed row i: the last s with cu[s] <= i, or -1 for a row
+// behind the last sequence.  Called by a whole warp.
+__device__ int find_sequence(const int32_t* cu, int n_seq, int64_t i, int lane);
+
 }  // namespace csa

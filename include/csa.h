@@ -413,6 +413,135 @@ int hca_shard_attend(const csa_params* p, int32_t batch, const void* q, const vo
 int attn_merge(const csa_params* p, int32_t batch, int32_t n_parts, const float* part_o, const float* part_ml,
                const float* sinks, void* out, csa_stream_t stream);
 
+/* ========================================================================
+ * Grouped-head attention over an uncompressed cache: the ordinary attention
+ * layers that stand beside the compressed ones.  H query heads share HK key /
+ * value heads (query head h reads key / value head h / (H / HK)); keys and
+ * values are separate.  A prompt is written with paged_append and attended
+ * with prompt_attn; each new token is written with paged_append and attended
+ * with paged_decode_attn.
+ *
+ * Paged cache: keys and values in pages of p->page_size tokens,
+ *   k_cache, v_cache: [n_pages][HK][page_size][d] in p->cache_fmt (FP8_S64:
+ *   codes, plus k_scales, v_scales float [n_pages][HK][page_size][d/64])
+ *   block_table: int32 [n_seq][max_pages]: token t of sequence s is row
+ *   t % page_size of page block_table[s][t / page_size].  Pages may be in any
+ *   order; entries of pages that a sequence does not use are not read.  A
+ *   page id outside [0, n_pages), or a token beyond max_pages pages, where one
+ *   is needed, sets CSA_DEV_BAD_INDEX: that token is not written, or is left
+ *   out of the attention.
+ * Strides: q, k and v rows of one token are [heads][d] dense; the rows of
+ * consecutive tokens are q_ld, k_ld, v_ld elements apart (>= heads * d, a
+ * multiple of 16 bytes), so that the slices of one fused projection's output
+ * are taken as they are.  Outputs are dense.
+ * Packed batches: the tokens of sequence s are rows cu[s] .. cu[s+1] - 1
+ * (cu: int32 [n_seq + 1], device, not decreasing, cu[0] = 0).  Rows from
+ * cu[n_seq] on (padding) are neither read for another row nor written.
+ * ======================================================================== */
+
+/* Parameters of the grouped-head calls.  H / HK <= 128; d 64, 128, 192 or
+ * 256.  cache_fmt is F32, BF16 or FP8_S64 (paged calls). */
+typedef struct csa_gqa_params {
+    int32_t n_heads;    /* H query heads */
+    int32_t n_kv_heads; /* HK key / value heads, a divisor of H */
+    int32_t head_dim;   /* d */
+    int32_t page_size;  /* tokens per page, >= 1 (paged calls) */
+    int32_t window;     /* W > 0: the token at t attends to t-W < i <= t; 0: to every i <= t */
+    int32_t rot_dim;    /* paged_append: leading dims that are rotated (a multiple of 16, 0..d) */
+    float scale;        /* softmax scale applied to q.k (not to the sink logit) */
+    int32_t act_fmt;    /* F32 or BF16: q, k, v and the outputs */
+    int32_t cache_fmt;
+    uint32_t flags;     /* CSA_FLAG_BATCH_INVARIANT (paged_decode_attn), CSA_FLAG_ROT_PAIRS */
+} csa_gqa_params;
+
+/* CSA_FLAG_ROT_PAIRS -- paged_append rotates neighbouring dims (2j, 2j+1)
+ *   instead of the dims j and j + rot_dim/2. */
+#define CSA_FLAG_ROT_PAIRS 0x8u
+
+/* Operations for csa_gqa_workspace_size. */
+#define CSA_OP_PAGED_DECODE 8
+#define CSA_OP_PROMPT_ATTN 9
+
+/* Bytes of workspace paged_decode_attn (n_seq = batch) or prompt_attn needs;
+ * 0 on bad arguments.  A workspace needs no initial contents; calls that may
+ * overlap need one each.  n_tokens: query tokens; n_ctx: rows that a sequence
+ * can hold (max_pages * page_size); both may be upper bounds. */
+size_t csa_gqa_workspace_size(const csa_gqa_params* p, int32_t op, int32_t n_seq, int64_t n_tokens,
+                              int64_t n_ctx);
+
+/* ------------------------------------------------------------------------
+ * paged_append -- rotate the new tokens' queries and keys by their position
+ * and append keys and values to the paged cache.  Token i of sequence s
+ * (packed row cu_q[s] + i) is at position t = pos0[s] + i.  With R = rot_dim
+ * and the pair (a, b) = (x[j], x[j + R/2]), j < R/2 (CSA_FLAG_ROT_PAIRS:
+ * (x[2j], x[2j+1])):
+ *   a' = a cos(t f_j) - b sin(t f_j),  b' = b cos(t f_j) + a sin(t f_j)
+ * in fp32, the angle reduced in fp64; dims from R on are copied.  Every result
+ * is rounded once: k' to act_fmt in k_out and from the same fp32 value to
+ * cache_fmt in the cache (FP8_S64 by the rule of csa_quantize).
+ *   q:         [n_tokens][H][d], token stride q_ld; NULL: no queries
+ *   k, v:      [n_tokens][HK][d], token strides k_ld, v_ld
+ *   cu_q:      int32 [n_seq + 1], or NULL: one token per sequence (n_tokens = n_seq)
+ *   pos0:      int64 [n_seq], the position of each sequence's first new token;
+ *              a sequence with pos0 < 0 is left out (nothing is written for it)
+ *   inv_freq:  double [rot_dim/2], f_j in radians per position (may be NULL
+ *              when rot_dim = 0)
+ *   q_out:     [n_tokens][H][d] in act_fmt (needed with q), may be q itself when
+ *              q is dense; k_out: [n_tokens][HK][d] or NULL, may be k itself
+ *              when k is dense
+ * Two tokens must not be at the same place of the cache.
+ * ------------------------------------------------------------------------ */
+int paged_append(const csa_gqa_params* p, int32_t n_seq, int64_t n_tokens, const int32_t* cu_q,
+                 const int64_t* pos0, const void* q, int64_t q_ld, const void* k, int64_t k_ld,
+                 const void* v, int64_t v_ld, const double* inv_freq, void* q_out, void* k_out,
+                 void* k_cache, float* k_scales, void* v_cache, float* v_scales, int64_t n_pages,
+                 const int32_t* block_table, int64_t max_pages, csa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * paged_decode_attn -- attention of one new token per sequence over the paged
+ * cache.  For sequence b at t = q_pos[b] (its own key and value already
+ * appended), over the visible tokens i:
+ *   l_i = scale * q.k_i,  M = max(sinks[h], max_i l_i)
+ *   out = sum_i e^(l_i-M) v_i / (sum_i e^(l_i-M) + e^(sinks[h]-M))
+ * (sinks == NULL: no sink term); a row without a visible token (t < 0) is 0.
+ * The cache is split over the GPU along its length and the parts are joined in
+ * a fixed order; with CSA_FLAG_BATCH_INVARIANT the parts of a row depend on
+ * its own length only.
+ *   q:         [batch][H][d] in act_fmt, row stride q_ld
+ *   q_pos:     int64 [batch]
+ *   sinks:     float [H] or NULL
+ *   out:       [batch][H][d] in act_fmt
+ *   workspace: >= csa_gqa_workspace_size(p, CSA_OP_PAGED_DECODE, batch, batch,
+ *              max_pages * page_size)
+ * ------------------------------------------------------------------------ */
+int paged_decode_attn(const csa_gqa_params* p, int32_t batch, const void* q, int64_t q_ld,
+                      const void* k_cache, const float* k_scales, const void* v_cache,
+                      const float* v_scales, int64_t n_pages, const int32_t* block_table,
+                      int64_t max_pages, const int64_t* q_pos, const float* sinks, void* out,
+                      void* workspace, size_t ws_bytes, csa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * prompt_attn -- causal attention over packed prompts.  Sequence s has the
+ * queries cu_q[s] .. cu_q[s+1]-1 and the keys cu_k[s] .. cu_k[s+1]-1, aligned
+ * at their ends: with len_q queries and len_k keys, query i stands at key
+ * position t = i + len_k - len_q and sees the keys j <= t (and j > t-W), by
+ * the softmax of paged_decode_attn.  For whole prompts cu_k is cu_q; a later
+ * chunk of a prompt has more keys than queries.  A query without a visible
+ * key (t < 0) gives 0.  Values and keys that a query does not see, infinities
+ * and NaN among them, do not reach its output.  p->page_size and p->cache_fmt
+ * are not used.
+ *   q:         [n_q][H][d] in act_fmt, token stride q_ld
+ *   k, v:      [n_k][HK][d] in act_fmt, token strides k_ld, v_ld
+ *   cu_q, cu_k: int32 [n_seq + 1]
+ *   sinks:     float [H] or NULL
+ *   out:       [n_q][H][d] in act_fmt
+ *   workspace: >= csa_gqa_workspace_size(p, CSA_OP_PROMPT_ATTN, n_seq, n_q, 0)
+ * ------------------------------------------------------------------------ */
+int prompt_attn(const csa_gqa_params* p, int32_t n_seq, const void* q, int64_t q_ld, int64_t n_q,
+                const void* k, int64_t k_ld, const void* v, int64_t v_ld, int64_t n_k,
+                const int32_t* cu_q, const int32_t* cu_k, const float* sinks, void* out,
+                void* workspace, size_t ws_bytes, csa_stream_t stream);
+
 /* Synchronise `stream`, return the device status word (CSA_DEV_* bits) in
  * *flags, and clear it if `reset` is non-zero.  The word is shared by every
  * call on the current device. */
