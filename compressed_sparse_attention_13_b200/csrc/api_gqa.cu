@@ -129,7 +129,8 @@ int prompt_attn(const csa_gqa_params* p, int32_t n_seq, const void* q, int64_t q
     a.H = p->n_heads; a.HK = p->n_kv_heads; a.D = p->head_dim; a.W = p->window; a.act_fmt = p->act_fmt;
     a.n_seq = n_seq; a.scale = p->scale; a.q = q; a.k = k; a.v = v; a.q_ld = q_ld; a.k_ld = k_ld; a.v_ld = v_ld;
     a.n_q = n_q; a.n_k = n_k; a.cu_q = cu_q; a.cu_k = cu_k; a.sinks = sinks; a.out = out;
-    return cuda_status(launch_prompt_simt(a, (cudaStream_t)stream));
+    return cuda_status(prompt_tc_supported(a) ? launch_prompt_tc(a, (cudaStream_t)stream)
+                                              : launch_prompt_simt(a, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -145,6 +145,8 @@ struct PromptArgs {
     void* out;                   // [n_q][H][D]
 };
 cudaError_t launch_prompt_simt(const PromptArgs& a, cudaStream_t s);
+bool prompt_tc_supported(const PromptArgs& a);
+cudaError_t launch_prompt_tc(const PromptArgs& a, cudaStream_t s);
 
 // The sequence of packed row i: the last s with cu[s] <= i, or -1 for a row
 // behind the last sequence.  Called by a whole warp.
