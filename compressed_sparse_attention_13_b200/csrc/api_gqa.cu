@@ -45,6 +45,9 @@ extern "C" {
 size_t csa_gqa_workspace_size(const csa_gqa_params* p, int32_t op, int32_t n_seq, int64_t n_tokens, int64_t n_ctx) {
     if (op != CSA_OP_PAGED_DECODE && op != CSA_OP_PROMPT_ATTN) return 0;
     if (check_gqa(p, op == CSA_OP_PAGED_DECODE) || n_seq < 0 || n_tokens < 0 || n_ctx < 0) return 0;
+    if (op == CSA_OP_PAGED_DECODE && paged_decode_tc_supported(p->act_fmt, p->cache_fmt))
+        return paged_decode_workspace(p->n_heads, p->n_kv_heads, p->head_dim, n_seq, n_ctx,
+                                      (p->flags & CSA_FLAG_BATCH_INVARIANT) != 0);
     return 256;
 }
 
@@ -94,7 +97,10 @@ int paged_decode_attn(const csa_gqa_params* p, int32_t batch, const void* q, int
     if ((st = check_ld(p, p->n_heads, q_ld))) return st;
     if ((st = check_cache(p, k_cache, k_scales, v_cache, v_scales, n_pages, block_table, max_pages))) return st;
     if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return CSA_ERR_ALIGN;
-    if (int64_t(batch) * p->n_heads > INT32_MAX) return CSA_ERR_UNSUPPORTED;
+    // cache rows, and the places of a sequence, are counted in 32 bits
+    if (int64_t(batch) * p->n_heads > INT32_MAX || max_pages * p->page_size > INT32_MAX ||
+        n_pages * p->n_kv_heads >= (int64_t(1) << 32) / p->page_size)
+        return CSA_ERR_UNSUPPORTED;
     if (ws_bytes < csa_gqa_workspace_size(p, CSA_OP_PAGED_DECODE, batch, batch, max_pages * p->page_size))
         return CSA_ERR_WORKSPACE;
     if (!workspace) return CSA_ERR_ARG;
@@ -104,7 +110,9 @@ int paged_decode_attn(const csa_gqa_params* p, int32_t batch, const void* q, int
     a.scale = p->scale; a.batch = batch; a.q = q; a.q_ld = q_ld; a.k_cache = k_cache; a.v_cache = v_cache;
     a.k_scales = k_scales; a.v_scales = v_scales; a.n_pages = n_pages; a.max_pages = max_pages;
     a.block_table = block_table; a.q_pos = q_pos; a.sinks = sinks; a.out = out;
-    return cuda_status(launch_paged_decode_simt(a, (cudaStream_t)stream));
+    return cuda_status(paged_decode_tc_supported(p->act_fmt, p->cache_fmt)
+                           ? launch_paged_decode_tc(a, workspace, (cudaStream_t)stream)
+                           : launch_paged_decode_simt(a, (cudaStream_t)stream));
 }
 
 int prompt_attn(const csa_gqa_params* p, int32_t n_seq, const void* q, int64_t q_ld, int64_t n_q,
