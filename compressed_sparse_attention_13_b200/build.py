@@ -1,8 +1,9 @@
 """Build libcsa13.so (the C-ABI library) with nvcc for sm_100a.
 
 Each .cu under csrc/ is compiled to an object in _build/ (relocatable device
-code, so every kernel shares the one device status word defined in api.cu),
-then nvcc links the shared library into this package directory.  Objects are
+code, so every kernel shares the one device status word defined in api.cu;
+the sources in WHOLE take its address as an argument instead), then nvcc links
+the shared library into this package directory.  Objects are
 rebuilt when their source or any header under csrc/ or include/ is newer.
 """
 from __future__ import annotations
@@ -25,6 +26,10 @@ FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-rdc=true", "-Xcompiler", "-fPIC",
          "--expt-relaxed-constexpr", "-Xptxas", "-warn-spills", f"-I{os.path.join(ROOT, 'include')}"]
 
 
+# Compiled as whole programs: in relocatable code ptxas ignores setmaxnreg.
+WHOLE = {"k_prompt_tc.cu"}
+
+
 def _headers():
     return glob.glob(os.path.join(CSRC, "**", "*.cuh"), recursive=True) + \
         glob.glob(os.path.join(CSRC, "**", "*.h"), recursive=True) + \
@@ -36,6 +41,8 @@ def _compile(src: str, hdr_mtime: float, verbose: bool) -> str:
     if os.path.exists(obj) and os.path.getmtime(obj) >= max(os.path.getmtime(src), hdr_mtime):
         return obj
     cmd = [NVCC, *ARCH, *FLAGS, "-c", src, "-o", obj]
+    if os.path.basename(src) in WHOLE:
+        cmd.remove("-rdc=true")
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
     r = subprocess.run(cmd, capture_output=True, text=True)

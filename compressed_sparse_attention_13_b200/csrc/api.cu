@@ -11,6 +11,11 @@ namespace csa {
 
 __device__ unsigned int g_status = 0;
 
+// (Asked of the runtime each time, a host-side table query: see noalloc.cu.)
+cudaError_t device_status_word(unsigned int** word) {
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_status);
+}
+
 cudaError_t ensure_smem_impl(const void* kernel, size_t bytes) {
     struct Entry { const void* k; int dev; size_t bytes; };
     static Entry table[64];

@@ -18,9 +18,14 @@ constexpr int kNumSMs = 148;  // B200
 constexpr int64_t kMaxGridY = 65535;  // largest grid extent along y (and z)
 
 // Device status word (CSA_DEV_* bits), shared by every call on a device.
+// Kernels compiled as whole programs (build.py) get its address from
+// device_status_word() as an argument.
+#ifdef __CUDACC_RDC__
 extern __device__ unsigned int g_status;
 
 __device__ __forceinline__ void flag_status(unsigned int bits) { atomicOr(&g_status, bits); }
+#endif
+cudaError_t device_status_word(unsigned int** word);  // of the current device
 
 // Programmatic dependent launch: a kernel launched with it may start before the
 // previous kernel of the stream has finished; pdl_wait() blocks until that

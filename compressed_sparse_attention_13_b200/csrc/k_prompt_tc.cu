@@ -7,30 +7,41 @@
 // the G query heads that share the head, so that a K / V tile serves all of
 // them and short sequences fill the rows.  A CTA owns NQ q tiles of
 // consecutive tokens (two for d <= 128, one above) and walks the keys that
-// any of its rows sees in tiles of BN, with the running maximum and sum of
+// any of its rows sees in tiles of 64, with the running maximum and sum of
 // each row in the thread that owns the row; P never leaves the SM.
 //
-//   S[row][key]  = Q (smem) . K^T (smem)    M = 128, N = BN, K = d    -> TMEM
-//   O[row][dim] += P (TMEM) . V (smem)      M = 128, N = d, K = BN    -> TMEM
+//   S[row][key]  = Q (smem) . K^T (smem)    M = 128, N = 64, K = d    -> TMEM
+//   O[row][dim] += P (TMEM) . V (smem)      M = 128, N = d, K = 64    -> TMEM
 //
-// P (bf16) overwrites the S columns it came from.  Per q tile (NQ = 2) or per
-// parity of the key tile (NQ = 1) there is one S slot, and the MMA thread
-// issues the product of one slot while the softmax works on the other: PV of
-// a slot, then the next QK into it (the tensor pipe runs them in order).
-// O is rescaled in TMEM only when a row's maximum has grown by more than 8
-// (log2 units) over the one in use.
+// P (bf16) overwrites the S columns it came from.  A q tile has two S slots, so
+// that S of the next key tile is there before the softmax is done with this
+// one: PV of a slot, then the next QK into it.  O is rescaled in TMEM only
+// when a row's maximum has grown by more than 8 (log2 units) over the one in
+// use.
 //
 // Roles: NQ warpgroups of softmax (thread = row; they also write the output),
-// then warp MMA (one thread issues), warp TMA (one thread loads q, K and V by
-// swizzled tensor copies; q rows of a tile are one box of G heads x tokens),
-// and two guard warps.  A tile that some row may not see completely is a
-// guarded one: before its PV the guard warps clear V rows past the sequence
-// (they belong to other sequences or are padding) and look for infinities and
-// NaN in the others, which a probability of 0 would not keep out of the sum.
-// If there are any, the CTA computes its rows once more, one key at a time
-// (attend_rows_slowly); that costs finite inputs only the look.
+// an MMA warp per q tile (one lane issues; two warps, so that one feeds the
+// tensor pipe under the other's waits: with one, 16,384 tokens took 12% more),
+// warp TMA (one lane loads q, K and V by swizzled tensor copies; q rows of a
+// tile are one box of G heads x tokens), and guard warps.  A tile that some
+// row may not see completely is a guarded one: before its PV the guard warps
+// clear V rows past the sequence (they belong to other sequences or are
+// padding) and look for infinities and NaN in those that some row does not
+// see: a probability of 0 would not keep them out of the sum.  They are
+// cleared too and their rows noted, and the epilogue adds them to the rows
+// that see them.
 //
-// Waits are bounded (sm100.cuh).
+// At d = 128 a pair of q tiles and 64 keys is 1024 clocks of MMA, about 1280 of
+// shared-memory reads for it (q is read again for every 64 keys) and, with 16
+// exponentials a clock, 1024 clocks of those; the softmax takes a quarter of
+// the exponentials by a polynomial on the FMA pipes (exp2_poly; none: 1% more
+// time at 16,384 tokens, half of them: 5% more).  Key tiles of 128 with one S
+// slot cost the same on one long prompt and 11% more on a packed batch of
+// short ones.  16,384 tokens, 32 heads over 8: 2.09 ms, 1.05 PFLOP/s, at the
+// board's power limit (1.57 GHz; 1.84 ms in the first milliseconds).
+//
+// Waits are bounded (sm100.cuh).  Compiled as a whole program: setmaxnreg
+// moves registers from the other warps to the softmax.
 #include <string.h>
 
 #include "kernels.h"
@@ -44,11 +55,17 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
+// Guarded tiles of a CTA of 256 consecutive tokens (the most: G = 1, NQ = 2) and
+// 64 keys a tile: its rows end inside at most 5 tiles, and with a window begin
+// inside at most 4.
+constexpr int kMaxGuarded = 9;
+
 template <int D>
 struct Cfg {
     static constexpr int NQ = D <= 128 ? 2 : 1;      // q tiles of a CTA
-    static constexpr int BN = D <= 128 ? 128 : 64;   // keys of a tile
-    static constexpr int NS = D == 64 ? 4 : D == 192 ? 3 : 2;  // stages of the K and of the V ring
+    static constexpr int BN = 64;                    // keys of a tile
+    static constexpr int kSlots = 2;                 // S slots of a q tile
+    static constexpr int NS = D <= 128 ? 4 : D == 192 ? 3 : 2;  // stages of the K and of the V ring
     static constexpr int kThreads = NQ * 128 + 128;
     static constexpr int kQBytes = 128 * D * 2;
     static constexpr int kTileBytes = BN * D * 2;
@@ -62,9 +79,11 @@ struct Smem {
     uint8_t v[C::NS][C::kTileBytes];
     uint64_t q_full[C::NQ], k_full[C::NS], k_empty[C::NS], v_full[C::NS], v_empty[C::NS];
     uint64_t g_full[C::NS], v_ok[C::NS];  // guarded tiles: landed, cleared
-    uint64_t s_full[2], p_full[2], o_done, o_full[C::NQ];
+    uint64_t s_full[2 * C::NQ], p_full[2 * C::NQ], o_done[2 * C::NQ], o_full[C::NQ], guard_done;
     uint32_t tmem_base;
     int seq, tile, bad;
+    uint32_t bad_rows[kMaxGuarded][C::BN / 32];  // guarded tiles' rows with non-finite values
+    int guarded_at[kMaxGuarded];                 // the guarded tiles' first keys
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -74,7 +93,9 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 __device__ __forceinline__ uint64_t pack2(float x, float y) {
-    return uint64_t(__float_as_uint(x)) | (uint64_t(__float_as_uint(y)) << 32);
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+    return v;
 }
 __device__ __forceinline__ float lo2(uint64_t v) { return __uint_as_float(uint32_t(v)); }
 __device__ __forceinline__ float hi2(uint64_t v) { return __uint_as_float(uint32_t(v >> 32)); }
@@ -104,53 +125,29 @@ struct Work {
     int kb0;           // first key of the first tile
 };
 
-// A row at a time, a key at a time, by one warp: what the tile path cannot do
-// (non-finite values among the keys that some rows do not see).
-template <int D>
-__device__ __noinline__ void attend_rows_slowly(const PromptArgs& a, const Work& w, int tok_begin, int rows, int G,
-                                                int lane) {
-    constexpr int E = D / 32;
-    for (int r = 0; r < rows; ++r) {
-        const int tok = tok_begin + r / G, h = w.hk * G + r % G;
-        if (tok >= w.len_q) break;
-        const int t = min(tok + w.off, w.nk - 1), lo = a.W > 0 ? max(tok + w.off - a.W + 1, 0) : 0;
-        float q[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            q[e] = bf16_bits_to_f32(((const uint16_t*)a.q)[(w.q0 + tok) * a.q_ld + int64_t(h) * D + lane + 32 * e]);
-            o[e] = 0.f;
-        }
-        for (int j = lo; j <= t; ++j) {
-            const uint16_t* kp = (const uint16_t*)a.k + (w.k0 + j) * a.k_ld + int64_t(w.hk) * D + lane;
-            const uint16_t* vp = (const uint16_t*)a.v + (w.k0 + j) * a.v_ld + int64_t(w.hk) * D + lane;
-            float x = 0.f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) x += q[e] * bf16_bits_to_f32(kp[32 * e]);
-            x = warp_sum(x) * (a.scale * kLog2e);
-            if (x == -INFINITY) continue;
-            if (x > m) {
-                const float al = m == -INFINITY ? 0.f : ex2(m - x);
-                l *= al;
-#pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = al == 0.f ? 0.f : o[e] * al;
-                m = x;
-            }
-            const float p = ex2(x - m);
-            l += p;
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] += p * bf16_bits_to_f32(vp[32 * e]);
-        }
-        float f = 1.f, den = l;
-        if (a.sinks) {
-            const float sg = a.sinks[h] * kLog2e, M = fmaxf(m, sg);
-            f = m == -INFINITY ? 0.f : ex2(m - M);
-            den = l * f + (M == -INFINITY ? 0.f : ex2(sg - M));
-        }
-        f = den == 0.f ? 0.f : f / den;
-        __nv_bfloat16* out = (__nv_bfloat16*)a.out + ((w.q0 + tok) * a.H + h) * int64_t(D) + lane;
-#pragma unroll
-        for (int e = 0; e < E; ++e) out[32 * e] = __float2bfloat16_rn(o[e] * f);
-    }
+// 2^y for two y <= 16, on the FMA and integer pipes: y = n + f with n the
+// integer below, 2^f by a cubic through f = 0 and 1 (the smallest largest
+// relative error, 1.0e-4, a twentieth of the rounding of P to bf16), n added to
+// the exponent.  y is raised to -127, where the result is 0; infinities and NaN
+// come out as anything (their rows are set to NaN as a whole).
+__device__ __forceinline__ uint64_t exp2_poly(uint64_t y) {
+    constexpr float kBig = 12582912.f;  // 1.5 * 2^23: its last place is 1
+    constexpr float c1 = 0.69542435f, c2 = 0.22630768f, c3 = 0.07826797f;
+    y = pack2(fmaxf(lo2(y), -127.f), fmaxf(hi2(y), -127.f));
+    uint64_t n, f, p;
+    asm("add.rm.f32x2 %0, %1, %2;" : "=l"(n) : "l"(y), "l"(pack2(kBig, kBig)));
+    f = add2(y, fma2(n, pack2(-1.f, -1.f), pack2(kBig, kBig)));
+    p = fma2(f, pack2(c3, c3), pack2(c2, c2));
+    p = fma2(f, p, pack2(c1, c1));
+    p = fma2(f, p, pack2(1.f, 1.f));
+    return pack2(__uint_as_float(__float_as_uint(lo2(p)) + (__float_as_uint(lo2(n)) << 23)),
+                 __uint_as_float(__float_as_uint(hi2(p)) + (__float_as_uint(hi2(n)) << 23)));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 }  // namespace
@@ -193,8 +190,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     Smem<D>& S = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kMma = NQ * 4, kTma = kMma + 1;
+    constexpr int kMma = NQ * 4, kTma = kMma + NQ, kGuards = 4 - NQ - 1;  // first warps, guard warps
     const int G = a.H / a.HK, tpt = 128 / G;  // tokens of a q tile
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_suspended<false>(bar, parity, a.status); };
+    auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_suspended<true>(bar, parity, a.status); };
 
     if (warp == 0) {
         int s, tile;
@@ -204,14 +203,19 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     if (threadIdx.x == 32) {
         for (int i = 0; i < NQ; ++i) { mbar_init(&S.q_full[i], 1); mbar_init(&S.o_full[i], 1); }
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&S.k_full[i], 1); mbar_init(&S.k_empty[i], 1);
-            mbar_init(&S.v_full[i], 1); mbar_init(&S.v_empty[i], 1);
+            mbar_init(&S.k_full[i], 1); mbar_init(&S.k_empty[i], NQ);  // one arrival per MMA warp
+            mbar_init(&S.v_full[i], 1); mbar_init(&S.v_empty[i], NQ);
             mbar_init(&S.g_full[i], 1);
-            mbar_init(&S.v_ok[i], 2);  // one arrival per guard warp
+            mbar_init(&S.v_ok[i], kGuards);  // one arrival per guard warp
         }
-        for (int i = 0; i < 2; ++i) { mbar_init(&S.s_full[i], 1); mbar_init(&S.p_full[i], 4); }
-        mbar_init(&S.o_done, 1);
+        for (int i = 0; i < 2 * NQ; ++i) {
+            mbar_init(&S.s_full[i], 1);
+            mbar_init(&S.o_done[i], 1);
+            mbar_init(&S.p_full[i], 4);  // one arrival per softmax warp of a tile
+        }
+        mbar_init(&S.guard_done, kGuards);
         S.bad = 0;
+        for (int i = 0; i < kMaxGuarded * BN / 32; ++i) (&S.bad_rows[0][0])[i] = 0;
         fence_mbar_init();
         prefetch_tmap(&map_q);
         prefetch_tmap(&map_k);
@@ -221,8 +225,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = S.tmem_base;
-    const uint32_t tO = tmem + 2 * BN;  // S slots at tmem + slot * BN, O of q tile i at tO + i * D
+    // All 512 columns are allocated, so they begin at column 0: a constant, which
+    // keeps the tensor instructions' addresses out of the registers.
+    constexpr uint32_t tmem = 0;
+    if (S.tmem_base != 0 && threadIdx.x == 0) atomicOr(a.status, CSA_DEV_TIMEOUT);
+    constexpr uint32_t tO = tmem + NQ * 128;  // S slots at tmem + slot * BN, O of q tile i at tO + i * D
 
     Work w;
     int n_t[NQ];    // key tiles of each q tile
@@ -247,7 +254,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             n_max = max(n_max, n_t[i]);
         }
         // a tile is guarded if some row of the CTA does not see all of it
-        const int t_first = w.tok0 + w.off, tok_last = min(w.tok0 + NQ * tpt, w.len_q) - 1;
+        const int t_first = min(w.tok0 + w.off, w.nk - 1), tok_last = min(w.tok0 + NQ * tpt, w.len_q) - 1;
         const int lo_last = a.W > 0 ? max(tok_last + w.off - a.W + 1, 0) : 0;
         auto guarded = [&](int j) {
             const int kb = w.kb0 + j * BN;
@@ -255,8 +262,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         };
 
         if (warp == kTma) {
-            if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-            if (lane == 0 && n_max > 0) {
+            if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+            if (elect_one() && n_max > 0) {
                 bool ok = true;
                 int nk_issued = 0, nq_issued = 0;
                 uint32_t v_par = 0, g_par = 0;  // bit st: parity of the phases begun on v_full, g_full
@@ -272,7 +279,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 for (int j = 0; j < n_max && ok; ++j) {
                     const int st = j % NS;
                     const int row = int(w.k0) + w.kb0 + j * BN;
-                    if (j >= NS) ok = mbar_wait(&S.k_empty[st], uint32_t((j / NS - 1) & 1));
+                    if (j >= NS) ok = wait(&S.k_empty[st], uint32_t((j / NS - 1) & 1));
                     if (!ok) break;
                     mbar_arrive_expect_tx(&S.k_full[st], C::kTileBytes);
 #pragma unroll
@@ -280,7 +287,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                         tma_load_3d(S.k[st] + blk * BN * 128, &map_k, 64 * blk, w.hk, row, &S.k_full[st]);
                     ++nk_issued;
                     if (NQ == 2 && j == 0 && n_t[NQ - 1] > 0) load_q(NQ - 1);
-                    if (j >= NS) ok = mbar_wait(&S.v_empty[st], uint32_t((j / NS - 1) & 1));
+                    if (j >= NS) ok = wait(&S.v_empty[st], uint32_t((j / NS - 1) & 1));
                     if (!ok) break;
                     uint64_t* full = guarded(j) ? &S.g_full[st] : &S.v_full[st];
                     mbar_arrive_expect_tx(full, C::kTileBytes);
@@ -292,127 +299,147 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 // every copy has landed before the CTA ends (already so unless a consumer gave up)
                 bool landed = true;
                 for (int i = 0; i < NQ && landed; ++i)
-                    if (nq_issued >> i & 1) landed = mbar_wait(&S.q_full[i], 0);
+                    if (nq_issued >> i & 1) landed = wait(&S.q_full[i], 0);
                 for (int j = max(0, nk_issued - NS); j < nk_issued && landed; ++j)
-                    landed = mbar_wait(&S.k_full[j % NS], uint32_t((j / NS) & 1));
+                    landed = wait(&S.k_full[j % NS], uint32_t((j / NS) & 1));
                 for (int st = 0; st < NS && landed; ++st)
-                    landed = mbar_wait(&S.v_full[st], (v_par >> st & 1) ^ 1) &&
-                             mbar_wait(&S.g_full[st], (g_par >> st & 1) ^ 1);
+                    landed = wait(&S.v_full[st], (v_par >> st & 1) ^ 1) &&
+                             wait(&S.g_full[st], (g_par >> st & 1) ^ 1);
             }
-        } else if (warp == kMma) {
-            if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-            if (lane == 0 && n_max > 0) {
-                const uint32_t id_qk = instr_desc(1, 1, 0, 0, 128, BN);
-                const uint32_t id_pv = instr_desc(1, 1, 0, 1, 128, D);  // V: keys x dims, MN-major
+        } else if (warp >= kMma && warp < kTma) {
+            if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+            if (n_max > 0) {
+                // The whole warp runs the loop (uniform registers hold what the instructions need), one lane issues.
+                constexpr uint32_t id_qk = instr_desc(1, 1, 0, 0, 128, BN);
+                constexpr uint32_t id_pv = instr_desc(1, 1, 0, 1, 128, D);  // V: keys x dims, MN-major
                 bool ok = true;
                 uint32_t v_par = 0, g_par = 0;  // bit st: parity of the next phase of v_full, v_ok
-                auto qk = [&](int i, int slot, int j) {
-                    const uint32_t q0 = smem_u32(S.q[i]), kk = smem_u32(S.k[j % NS]);
-#pragma unroll
-                    for (int s = 0; s < D / 16; ++s)
-                        mma_f16(tmem + slot * BN, smem_desc(q0 + (s >> 2) * 16384 + (s & 3) * 32, 16, 1024),
-                                smem_desc(kk + (s >> 2) * BN * 128 + (s & 3) * 32, 16, 1024), id_qk, s != 0);
-                    mma_commit(&S.s_full[slot]);
+                // descriptors count addresses in units of 16 bytes; offsets are added to a base
+                const uint64_t d_q = smem_desc(smem_u32(S.q[0]), 16, 1024), d_k = smem_desc(smem_u32(S.k[0]), 16, 1024),
+                               d_v = smem_desc(smem_u32(S.v[0]), BN * 128, 1024);
+                auto commit = [&](uint64_t* bar) {
+                    if (elect_one()) mma_commit(bar);
                 };
-                auto pv = [&](int i, int slot, int j) {
-                    const uint32_t vv = smem_u32(S.v[j % NS]);
+                const int i = warp - kMma, n = n_t[i];
+                auto qk = [&](int slot, int st) {
+                    if (elect_one()) {
+                        const uint64_t q0 = d_q + uint32_t(i * (C::kQBytes / 16)), kk = d_k + uint32_t(st * (C::kTileBytes / 16));
 #pragma unroll
-                    for (int s = 0; s < BN / 16; ++s)
-                        mma_f16_ts(tO + i * D, tmem + slot * BN + 8 * s,
-                                   smem_desc(vv + s * 2048, BN * 128, 1024), id_pv, (j | s) != 0);
+                        for (int s = 0; s < D / 16; ++s)
+                            mma_f16(tmem + slot * BN, q0 + (s >> 2) * 1024 + (s & 3) * 2,
+                                    kk + (s >> 2) * BN * 8 + (s & 3) * 2, id_qk, s != 0);
+                        mma_commit(&S.s_full[slot]);
+                    }
                 };
-                auto wait_v = [&](int j) {
-                    const int st = j % NS;
+                auto pv = [&](int slot, int st, bool first, uint64_t* done) {
+                    if (elect_one()) {
+                        const uint64_t vv = d_v + uint32_t(st * (C::kTileBytes / 16));
+#pragma unroll
+                        for (int s = 0; s < BN / 16; ++s)
+                            mma_f16_ts(tO + i * D, tmem + slot * BN + 8 * s, vv + s * 128, id_pv, !first || s != 0);
+                        mma_commit(done);
+                    }
+                };
+                auto wait_v = [&](int j, int st) {
                     const bool g = guarded(j);
                     uint32_t& par = g ? g_par : v_par;
                     const uint32_t p = par >> st & 1;
                     par ^= 1u << st;
-                    return mbar_wait(g ? &S.v_ok[st] : &S.v_full[st], p);
+                    return wait_warp(g ? &S.v_ok[st] : &S.v_full[st], p);
                 };
-                auto wait_k = [&](int j) { return mbar_wait(&S.k_full[j % NS], uint32_t((j / NS) & 1)); };
-                if constexpr (NQ == 2) {
-                    ok = wait_k(0);
-                    for (int i = 0; i < 2 && ok; ++i)
-                        if (n_t[i] > 0) {
-                            ok = mbar_wait(&S.q_full[i], 0);
-                            if (ok) qk(i, i, 0);
-                        }
-                    if (ok) mma_commit(&S.k_empty[0]);
-                    for (int j = 0; j < n_max && ok; ++j) {
-                        ok = wait_v(j);
-                        bool have_k = false;
-                        for (int i = 0; i < 2 && ok; ++i) {
-                            if (j < n_t[i]) {
-                                ok = mbar_wait(&S.p_full[i], uint32_t(j & 1));
-                                if (!ok) break;
-                                tc_fence_after();
-                                pv(i, i, j);
-                                if (j == n_t[i] - 1) mma_commit(&S.o_full[i]);
-                            }
-                            if (j + 1 < n_t[i]) {
-                                if (!have_k) { ok = wait_k(j + 1); have_k = true; }
-                                if (ok) qk(i, i, j + 1);
-                            }
-                        }
-                        if (!ok) break;
-                        mma_commit(&S.v_empty[j % NS]);
-                        if (j + 1 < n_max) mma_commit(&S.k_empty[(j + 1) % NS]);
-                    }
-                } else {
-                    ok = wait_k(0) && mbar_wait(&S.q_full[0], 0);
-                    if (ok) { qk(0, 0, 0); mma_commit(&S.k_empty[0]); }
-                    if (ok && n_max > 1) {
-                        ok = wait_k(1);
-                        if (ok) { qk(0, 1, 1); mma_commit(&S.k_empty[1 % NS]); }
-                    }
-                    for (int j = 0; j < n_max && ok; ++j) {
-                        ok = wait_v(j) && mbar_wait(&S.p_full[j & 1], uint32_t((j >> 1) & 1));
+                // S of the first key tiles, then by tile: PV of it, S of the one that comes into its slot.
+                // K and V of the next round are waited for before its P is: only that wait is in the chain.
+                int st = 0, st2 = 0;       // stages of the tiles j and j + kSlots
+                uint32_t k_par = 0;        // parity of k_full[st2]
+                auto wait_k = [&]() { return wait_warp(&S.k_full[st2], k_par); };
+                auto next_k = [&]() {
+                    commit(&S.k_empty[st2]);
+                    if (++st2 == NS) { st2 = 0; k_par ^= 1; }
+                };
+                ok = wait_warp(&S.q_full[0], 0);
+                if (ok && i > 0 && n > 0) ok = wait_warp(&S.q_full[i], 0);
+                for (int j = 0; j < C::kSlots && j < n_max && ok; ++j) {
+                    ok = wait_k();
+                    if (!ok) break;
+                    if (j < n) qk(C::kSlots * i + j, st2);
+                    next_k();
+                }
+                if (ok && C::kSlots < n_max) ok = wait_k();
+                if (ok) ok = wait_v(0, 0);
+                for (int j = 0; j < n_max && ok; ++j) {
+                    const int slot = C::kSlots * i + j % C::kSlots;
+                    if (j < n) {
+                        ok = wait_warp(&S.p_full[slot], uint32_t(j / C::kSlots & 1));
                         if (!ok) break;
                         tc_fence_after();
-                        pv(0, j & 1, j);
-                        mma_commit(&S.v_empty[j % NS]);
-                        mma_commit(&S.o_done);
-                        if (j == n_max - 1) mma_commit(&S.o_full[0]);
-                        if (j + 2 < n_max) {
-                            ok = wait_k(j + 2);
-                            if (ok) { qk(0, j & 1, j + 2); mma_commit(&S.k_empty[(j + 2) % NS]); }
-                        }
+                        pv(slot, st, j == 0, j == n - 1 ? &S.o_full[i] : &S.o_done[slot]);
+                        if (j + C::kSlots < n) qk(slot, st2);
                     }
+                    commit(&S.v_empty[st]);
+                    if (++st == NS) st = 0;
+                    if (j + C::kSlots < n_max) {
+                        next_k();
+                        if (j + 1 + C::kSlots < n_max) ok = wait_k();
+                    }
+                    if (ok && j + 1 < n_max) ok = wait_v(j + 1, st);
                 }
             }
         } else if (warp > kTma) {
-            if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+            if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
             // ------------------------------------------------------- guard
-            const int gt = threadIdx.x - (kTma + 1) * 32;  // 0..63
+            const int gt = threadIdx.x - (kTma + 1) * 32;  // 0 .. 32 kGuards - 1
             bool ok = true;
             uint32_t g_par = 0;
+            int nth = 0;
+            const __nv_bfloat162 zero2 = __floats2bfloat162_rn(0.f, 0.f);
             for (int j = 0; j < n_max && ok; ++j) {
                 if (!guarded(j)) continue;
                 const int st = j % NS, kb = w.kb0 + j * BN;
-                ok = mbar_wait(&S.g_full[st], g_par >> st & 1);
+                ok = wait_warp(&S.g_full[st], g_par >> st & 1);
                 if (!ok) break;
                 g_par ^= 1u << st;
-                bool bad = false;
-                const int live = w.nk - kb;  // rows of the tile that exist
-                for (int c = gt; c < C::kTileBytes / 16; c += 64) {
-                    uint4* p = reinterpret_cast<uint4*>(S.v[st]) + c;
-                    if ((c >> 3) % BN >= live) {
-                        *p = make_uint4(0, 0, 0, 0);
-                    } else {
-                        const uint4 x = *p;
-                        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+                const int live = min(w.nk - kb, BN);  // rows of the tile that exist
+                // of those, [seen0, seen1) are seen by every row
+                const int seen0 = max(lo_last - kb, 0), seen1 = t_first + 1 - kb;
+                if (gt == 0) S.guarded_at[nth] = kb;
+                uint4* const v = reinterpret_cast<uint4*>(S.v[st]);
+                // row r's chunks are in their swizzled order, all are looked at
+                for (int r = gt; r < BN; r += 32 * kGuards) {
+                    if (r >= live) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            bad |= (y[i] & 0x7F80u) == 0x7F80u || (y[i] & 0x7F800000u) == 0x7F800000u;
+                        for (int c = 0; c < D / 8; ++c) v[(c >> 3) * BN * 8 + r * 8 + ((c ^ r) & 7)] = make_uint4(0, 0, 0, 0);
+                    } else if (r < seen0 || r >= seen1) {
+                        __nv_bfloat162 acc[4] = {zero2, zero2, zero2, zero2};  // NaN from any value that is not finite
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c) {
+                            const uint4 x = v[(c >> 3) * BN * 8 + r * 8 + ((c ^ r) & 7)];
+                            acc[0] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.x), zero2, acc[0]);
+                            acc[1] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.y), zero2, acc[1]);
+                            acc[2] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.z), zero2, acc[2]);
+                            acc[3] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.w), zero2, acc[3]);
+                        }
+                        const __nv_bfloat162 all = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
+                        const float2 sum = __bfloat1622float2(all);
+                        if (sum.x + sum.y != 0.f) {  // (NaN)
+                            uint16_t* const e = reinterpret_cast<uint16_t*>(S.v[st]);
+                            for (int i = 0; i < D; ++i) {
+                                uint16_t* const p = e + (i >> 6) * BN * 64 + r * 64 + (i & 63);
+                                if ((*p & 0x7F80) == 0x7F80) *p = 0;
+                            }
+                            atomicOr(&S.bad_rows[nth][r >> 5], 1u << (r & 31));
+                            S.bad = 1;
+                        }
                     }
                 }
-                if (bad) S.bad = 1;
+                ++nth;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&S.v_ok[st]);
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.guard_done);  // S.bad and its rows are complete
         } else {
-            if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+            if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
             // ----------------------------------------------------- softmax
             const int i = warp >> 2, r = threadIdx.x & 127;
             const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
@@ -420,47 +447,49 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             const bool live = r < G * tpt && tok < w.len_q;
             const int t = live ? min(tok + w.off, w.nk - 1) : -1;       // last key that the row sees
             const int lo = a.W > 0 ? max(tok + w.off - a.W + 1, 0) : 0;  // first
-            const int t_min = w.tok0 + i * tpt + w.off;                   // of the tile's first token
+            const int t_min = min(w.tok0 + i * tpt + w.off, w.nk - 1);    // of the tile's first token
             const int tl = min(w.tok0 + (i + 1) * tpt, w.len_q) - 1;
             const int lo_max = a.W > 0 ? max(tl + w.off - a.W + 1, 0) : 0;
             const float sl2 = a.scale * kLog2e;
+            const uint64_t s2 = pack2(sl2, sl2);
             float m = -INFINITY, l = 0.f;
             bool ok = true;
             const int n = n_t[i];
             for (int j = 0; j < n && ok; ++j) {
-                const int slot = NQ == 2 ? i : (j & 1);
-                ok = mbar_wait(&S.s_full[slot], uint32_t((NQ == 2 ? j : j >> 1) & 1));
+                const int slot = C::kSlots * i + j % C::kSlots;
+                ok = wait_warp(&S.s_full[slot], uint32_t(j / C::kSlots & 1));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t tS = tmem + slot * BN + lanes;
-                uint32_t x[BN / 32][32];
-#pragma unroll
-                for (int c = 0; c < BN / 32; ++c) tmem_ld32_start(tS + 32 * c, x[c]);
-#pragma unroll
-                for (int c = 0; c < BN / 32; ++c) tmem_wait_ld32(x[c]);
                 const int kb = w.kb0 + j * BN;
+                constexpr int NC = BN / 32;
+                uint32_t x[NC][32];
+#pragma unroll
+                for (int c = 0; c < NC; ++c) tmem_ld32_start(tS + 32 * c, x[c]);
+#pragma unroll
+                for (int c = 0; c < NC; ++c) tmem_wait_ld32(x[c]);
                 if (kb + BN - 1 > t_min || kb < lo_max) {
-                    // columns [lo - kb, t - kb] of this row are visible
-                    const int c1 = t - kb, c0 = lo - kb;
+                    // of this row's columns [lo - kb, t - kb] are visible
 #pragma unroll
                     for (int c = 0; c < BN; ++c)
-                        if (c > c1 || c < c0) x[c / 32][c % 32] = 0xFF800000u;
+                        if (c > t - kb || c < lo - kb) x[c / 32][c % 32] = 0xFF800000u;
                 }
                 float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < BN; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], __uint_as_float(x[c / 32][c % 32]));
-                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
+                for (int c = 0; c < BN; c += 2)
+                    mx4[c / 2 & 3] = max3(mx4[c / 2 & 3], __uint_as_float(x[c / 32][c % 32]), __uint_as_float(x[c / 32][c % 32 + 1]));
+                const float mx = max3(mx4[0], mx4[1], max3(mx4[2], mx4[3], -INFINITY)) * sl2;
+                if (!(mx < INFINITY)) l = __int_as_float(0x7FFFFFFF);  // NaN or +inf among the logits: the row is NaN
                 float al = 1.f;
-                if (mx > m + kRescaleThreshold || (m == -INFINITY && mx != -INFINITY)) {
+                if (mx > m + kRescaleThreshold || (m == -INFINITY && mx > -INFINITY)) {
                     al = m == -INFINITY ? 0.f : ex2(m - mx);
                     m = mx;
                 }
                 if (__any_sync(0xffffffffu, al != 1.f) && j > 0) {
-                    if (NQ == 1) {  // (NQ = 2: the S tile's commit came after the last PV's)
-                        ok = mbar_wait(&S.o_done, uint32_t((j - 1) & 1));
-                        if (!ok) break;
-                        tc_fence_after();
-                    }
+                    // (PV of the tile before is waited for here only)
+                    ok = wait_warp(&S.o_done[slot ^ (C::kSlots - 1)], uint32_t((j - 1) / C::kSlots & 1));
+                    if (!ok) break;
+                    tc_fence_after();
                     const uint32_t ad = tO + i * D + lanes;
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
@@ -474,27 +503,26 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 }
                 l *= al;
                 const float neg = m == -INFINITY ? 0.f : -m;
-                const uint64_t s2 = pack2(sl2, sl2), n2 = pack2(neg, neg);
+                const uint64_t n2 = pack2(neg, neg);
                 uint64_t sum[2] = {0, 0};
 #pragma unroll
-                for (int c = 0; c < BN / 32; c += 2) {
-                    uint32_t p[32];
+                for (int c = 0; c < NC; ++c) {
+                    uint32_t p[16];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const int k = 32 * c + 2 * e;
-                        const uint64_t y = fma2(pack2(__uint_as_float(x[k / 32][k % 32]), __uint_as_float(x[k / 32][k % 32 + 1])), s2, n2);
-                        const float p0 = ex2(lo2(y)), p1 = ex2(hi2(y));
-                        sum[e & 1] = add2(sum[e & 1], pack2(p0, p1));
-                        p[e] = bf16x2(p0, p1);
+                    for (int e = 0; e < 16; ++e) {
+                        const uint64_t y = fma2(pack2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), s2, n2);
+                        const uint64_t z = (e & 3) == 3 ? exp2_poly(y) : pack2(ex2(lo2(y)), ex2(hi2(y)));
+                        sum[e & 1] = add2(sum[e & 1], z);
+                        p[e] = bf16x2(lo2(z), hi2(z));
                     }
-                    tmem_st32(tS + 16 * c, p);
+                    tmem_st16(tS + 16 * c, p);
                 }
-                sum[0] = add2(sum[0], sum[1]);
-                l += lo2(sum[0]) + hi2(sum[0]);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&S.p_full[slot]);
+                sum[0] = add2(sum[0], sum[1]);
+                l += lo2(sum[0]) + hi2(sum[0]);
             }
             // ---------------------------------------------------- epilogue
             float f = 1.f, den = l;
@@ -504,7 +532,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 den = l * f + (M == -INFINITY ? 0.f : ex2(sg - M));
             }
             f = den == 0.f ? 0.f : f / den;
-            if (n > 0 && ok) ok = mbar_wait(&S.o_full[i], 0);
+            if (n > 0 && ok) ok = wait_warp(&S.o_full[i], 0) && wait_warp(&S.guard_done, 0);
             tc_fence_after();
             __nv_bfloat16* out = (__nv_bfloat16*)a.out + ((w.q0 + tok) * a.H + h) * int64_t(D);
 #pragma unroll 1
@@ -516,6 +544,19 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = 0;
+                }
+                if (S.bad) {  // the non-finite values that this row sees (they came out of the tiles as 0)
+                    for (int x = 0; x < kMaxGuarded * BN; ++x) {
+                        if (!(S.bad_rows[x / BN][x % BN / 32] >> (x % 32) & 1)) continue;
+                        const int key = S.guarded_at[x / BN] + x % BN;
+                        if (key < lo || key > t) continue;
+                        const uint16_t* vp = (const uint16_t*)a.v + (w.k0 + key) * a.v_ld + int64_t(w.hk) * D + 32 * c;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float y = bf16_bits_to_f32(vp[e]);
+                            if (!(fabsf(y) < INFINITY)) o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
+                        }
+                    }
                 }
                 if (live) {
 #pragma unroll
@@ -534,14 +575,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     if (warp == kMma) tmem_dealloc(tmem, 512);
-    // Non-finite values in a guarded tile: each softmax warp redoes 32 rows of
-    // its tile from memory (the barrier has ordered the first results' writes).
-    if (seq >= 0 && S.bad && warp < kMma) {
-        const int tile = warp >> 2, part = (tpt + 3) / 4;
-        const int first = w.tok0 + tile * tpt + (warp & 3) * part;
-        const int n = min(part, tpt - (warp & 3) * part);
-        if (n > 0) attend_rows_slowly<D>(a, w, first, n * G, G, lane);
-    }
 }
 
 bool prompt_tc_supported(const PromptArgs& a) {
@@ -550,7 +583,7 @@ bool prompt_tc_supported(const PromptArgs& a) {
 }
 
 template <int D>
-static cudaError_t launch_prompt_tc_d(const PromptArgs& a, cudaStream_t s) {
+static cudaError_t launch_prompt_tc_d(PromptArgs a, cudaStream_t s) {
     using C = Cfg<D>;
     const int G = a.H / a.HK, tpt = 128 / G;
     CUtensorMap mq, mk, mv;
@@ -566,7 +599,8 @@ static cudaError_t launch_prompt_tc_d(const PromptArgs& a, cudaStream_t s) {
         !encode_tile_map(&mv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.v, dk, sv, bk, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
     const size_t sm = sizeof(Smem<D>) + 1024;
-    const cudaError_t e = ensure_smem(prompt_tc_kernel<D>, sm);
+    cudaError_t e = ensure_smem(prompt_tc_kernel<D>, sm);
+    if (e == cudaSuccess) e = device_status_word(&a.status);
     if (e != cudaSuccess) return e;
     // an upper bound of the tiles: the lengths are on the device
     const int64_t tiles = a.n_q / (C::NQ * tpt) + std::min<int64_t>(a.n_seq, a.n_q);

@@ -146,6 +146,7 @@ struct PromptArgs {
     const int32_t *cu_q, *cu_k;  // [n_seq + 1]
     const float* sinks;          // [H] or null
     void* out;                   // [n_q][H][D]
+    unsigned int* status;        // device status word (set by the launcher that needs it)
 };
 cudaError_t launch_prompt_simt(const PromptArgs& a, cudaStream_t s);
 bool prompt_tc_supported(const PromptArgs& a);

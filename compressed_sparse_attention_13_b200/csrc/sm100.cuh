@@ -75,17 +75,58 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Wait for the phase with the given parity to complete.  Returns false (and
-// flags CSA_DEV_TIMEOUT) if it does not within kWaitNs.
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
+// Wait for the phase with the given parity to complete.  Returns false if it
+// does not within kWaitNs.
+__device__ __forceinline__ bool mbar_wait_unflagged(uint64_t* bar, uint32_t parity) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_ns();
     for (uint32_t i = 1;; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
         if ((i & 255u) == 0 && global_ns() - t0 > kWaitNs) break;
     }
+    return false;
+}
+
+// The same, flagging CSA_DEV_TIMEOUT when it gives up.
+#ifdef __CUDACC_RDC__
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
+    if (mbar_wait_unflagged(bar, parity)) return true;
     flag_status(CSA_DEV_TIMEOUT);
     return false;
+}
+#endif
+// For kernels whose warps wait long beside others that compute: the thread is
+// suspended for up to 20 us a try instead of polling.  WARP: a converged warp
+// waits; its lanes go on together.
+template <bool WARP>
+__device__ __forceinline__ bool mbar_wait_suspended(uint64_t* bar, uint32_t parity, unsigned int* status) {
+    uint64_t t0 = 0;
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n"
+            " mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n"
+            " selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+            : "memory");
+        if (WARP ? __all_sync(0xffffffffu, ok) : ok) return true;
+        const uint64_t t = global_ns();
+        if (t0 == 0) t0 = t;
+        if (WARP ? __any_sync(0xffffffffu, t - t0 > kWaitNs) : t - t0 > kWaitNs) break;
+    }
+    atomicOr(status, CSA_DEV_TIMEOUT);
+    return false;
+}
+
+// One lane of a converged warp, the same each time.  Under a branch on it the
+// compiler knows that a single lane runs and moves operands of tensor
+// instructions to uniform registers directly (under `lane == 0` it emits a
+// loop over the lanes' values, about 50 clocks for each instruction).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+    return r != 0;
 }
 
 // Fetch a tensor map (a __grid_constant__ kernel parameter) into the TMA
@@ -286,6 +327,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
