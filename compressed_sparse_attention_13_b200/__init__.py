@@ -319,9 +319,23 @@ def empty_paged(p: GqaParams, n_pages: int, device="cuda"):
     return tuple(caches)
 
 
+# These calls launch kernels of a few microseconds: their checks go by plain
+# integers and by torch's own comparisons (a device object or a Stream costs a
+# microsecond or more to make).
+_dtypes = {}
+
+
+def _dtype(fmt):
+    """The torch type that elements of a format are passed in."""
+    if not _dtypes:
+        import torch
+        _dtypes.update({F32: torch.float32, BF16: torch.bfloat16, FP8_S64: torch.uint8, "i32": torch.int32,
+                        "i64": torch.int64, "f64": torch.float64})
+    return _dtypes[fmt]
+
+
 def _act_dtype(p):
-    import torch
-    return torch.float32 if p.act_fmt == F32 else torch.bfloat16
+    return _dtype(F32 if p.act_fmt == F32 else BF16)
 
 
 def _rows_of(t, n, heads, p, name):
@@ -330,9 +344,9 @@ def _rows_of(t, n, heads, p, name):
     d = p.head_dim
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
-    if t.dtype != _act_dtype(p):
-        raise ValueError(f"{name} must be {_act_dtype(p)}, got {t.dtype}")
-    if tuple(t.shape) != (n, heads, d):
+    if t.dtype != (act := _act_dtype(p)):
+        raise ValueError(f"{name} must be {act}, got {t.dtype}")
+    if t.shape != (n, heads, d):
         raise ValueError(f"{name} must be [{n}][{heads}][{d}], got {list(t.shape)}")
     s = t.stride()
     if s[2] != 1 or (heads > 1 and s[1] != d):
@@ -344,91 +358,84 @@ def _dense(t, shape, dtype, name):
     """Pointer of a dense tensor of this shape and type (None: no tensor)."""
     if t is None:
         return None
-    if tuple(t.shape) != shape or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
     return _p(t)
 
 
 def _caches(p, k_cache, v_cache, block_table, n_seq):
-    import torch
-    n_pages = k_cache.data.shape[0]
-    lead = (n_pages, p.n_kv_heads, p.page_size)
-    fp8 = p.cache_fmt == FP8_S64
-    dtype = {F32: torch.float32, BF16: torch.bfloat16}.get(p.cache_fmt, torch.uint8)
+    n_pages, hk, page, d = k_cache.data.shape[0], p.n_kv_heads, p.page_size, p.head_dim
+    fmt = p.cache_fmt
+    dtype = _dtype(fmt if fmt in (F32, BF16) else FP8_S64)
     ptrs = []
     for st, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if st.fmt != p.cache_fmt:
-            raise ValueError(f"{name} is stored in format {st.fmt}, the parameters name {p.cache_fmt}")
-        ptrs.append(_dense(st.data, lead + (p.head_dim,), dtype, name))
-        ptrs.append(_dense(st.scales, lead + (p.head_dim // 64,), torch.float32, name + " scales") if fp8 else None)
+        if st.fmt != fmt:
+            raise ValueError(f"{name} is stored in format {st.fmt}, the parameters name {fmt}")
+        ptrs.append(_dense(st.data, (n_pages, hk, page, d), dtype, name))
+        ptrs.append(_dense(st.scales, (n_pages, hk, page, d // 64), _dtype(F32), name + " scales")
+                    if fmt == FP8_S64 else None)
     if block_table.dim() != 2 or block_table.shape[0] != n_seq:
         raise ValueError(f"block_table must be [{n_seq}][max_pages], got {list(block_table.shape)}")
     max_pages = block_table.shape[1]
-    table = _dense(block_table, (n_seq, max_pages), torch.int32, "block_table")
+    table = _dense(block_table, (n_seq, max_pages), _dtype("i32"), "block_table")
     return (*ptrs, n_pages, table, max_pages)
 
 
-class _On:
-    """Makes the device of `t` current for a call (launches and the default
-    stream go by the current device) and refuses tensors of another one."""
-
-    def __init__(self, t, *others):
-        import torch
-        for o in others:
-            if o is not None and o.device != t.device:
-                raise ValueError(f"tensors on different devices: {t.device}, {o.device}")
-        self.guard = None if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *e):
-        if self.guard is not None:
-            self.guard.__exit__(*e)
+def _launch(fn, p, n, args, stream, t, *others):
+    """Call an entry point with the device of `t` current (launches and the default stream go by
+    the current device); tensors of another device are refused."""
+    import torch
+    dev = t.get_device()
+    for o in others:
+        if o is not None and o.get_device() != dev:
+            raise ValueError(f"tensors on different devices: {t.device}, {o.device}")
+    call = getattr(_lib or lib(), fn)
+    if dev == torch.cuda.current_device():
+        s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+        _ok(fn, call(C.byref(p), n, *args, s))
+    else:
+        with torch.cuda.device(dev):
+            _ok(fn, call(C.byref(p), n, *args, _s(stream)))
 
 
 def paged_append(p: GqaParams, n_seq: int, n_tokens: int, cu_q, pos0, q, k, v, inv_freq, q_out, k_out,
                  k_cache: Stored, v_cache: Stored, block_table, stream=None):
     """q [n_tokens][H][d] (or None), k, v [n_tokens][HK][d]; cu_q int32 [n_seq + 1] or None
     (one token per sequence); pos0 int64 [n_seq]; inv_freq float64 [rot_dim / 2] or None."""
-    import torch
     H, HK, d, act = p.n_heads, p.n_kv_heads, p.head_dim, _act_dtype(p)
     qp, ql = _rows_of(q, n_tokens, H, p, "q") if q is not None else (None, 0)
     kp, kl = _rows_of(k, n_tokens, HK, p, "k")
     vp, vl = _rows_of(v, n_tokens, HK, p, "v")
-    args = (_dense(cu_q, (n_seq + 1,), torch.int32, "cu_q"), _dense(pos0, (n_seq,), torch.int64, "pos0"), qp, ql, kp,
-            kl, vp, vl, _dense(inv_freq, (p.rot_dim // 2,), torch.float64, "inv_freq") if p.rot_dim > 0 else None,
+    rot = p.rot_dim
+    args = (n_tokens, _dense(cu_q, (n_seq + 1,), _dtype("i32"), "cu_q"), _dense(pos0, (n_seq,), _dtype("i64"), "pos0"),
+            qp, ql, kp, kl, vp, vl, _dense(inv_freq, (rot // 2,), _dtype("f64"), "inv_freq") if rot > 0 else None,
             _dense(q_out, (n_tokens, H, d), act, "q_out"), _dense(k_out, (n_tokens, HK, d), act, "k_out"),
             *_caches(p, k_cache, v_cache, block_table, n_seq))
-    with _On(k, q, v, cu_q, pos0, inv_freq, q_out, k_out, k_cache.data, v_cache.data, block_table):
-        _ok("paged_append", lib().paged_append(C.byref(p), n_seq, n_tokens, *args, _s(stream)))
+    _launch("paged_append", p, n_seq, args, stream, k, q, v, cu_q, pos0, inv_freq, q_out, k_out, k_cache.data,
+            k_cache.scales, v_cache.data, v_cache.scales, block_table)
 
 
 def paged_decode_attn(p: GqaParams, batch: int, q, k_cache: Stored, v_cache: Stored, block_table, q_pos, sinks,
                       out, workspace, stream=None):
     """q, out [batch][H][d]; q_pos int64 [batch]; sinks float32 [H] or None."""
-    import torch
     qp, ql = _rows_of(q, batch, p.n_heads, p, "q")
     wp, wb = _ws(workspace)
-    args = (qp, ql, *_caches(p, k_cache, v_cache, block_table, batch), _dense(q_pos, (batch,), torch.int64, "q_pos"),
-            _dense(sinks, (p.n_heads,), torch.float32, "sinks"),
+    args = (qp, ql, *_caches(p, k_cache, v_cache, block_table, batch), _dense(q_pos, (batch,), _dtype("i64"), "q_pos"),
+            _dense(sinks, (p.n_heads,), _dtype(F32), "sinks"),
             _dense(out, (batch, p.n_heads, p.head_dim), _act_dtype(p), "out"), wp, wb)
-    with _On(q, k_cache.data, v_cache.data, block_table, q_pos, sinks, out, workspace):
-        _ok("paged_decode_attn", lib().paged_decode_attn(C.byref(p), batch, *args, _s(stream)))
+    _launch("paged_decode_attn", p, batch, args, stream, q, k_cache.data, k_cache.scales, v_cache.data, v_cache.scales,
+            block_table, q_pos, sinks, out, workspace)
 
 
 def prompt_attn(p: GqaParams, n_seq: int, q, k, v, cu_q, cu_k, sinks, out, workspace, stream=None):
     """q, out [n_q][H][d], k, v [n_k][HK][d]; cu_q, cu_k int32 [n_seq + 1]; sinks float32 [H]
     or None."""
-    import torch
     n_q, n_k = q.shape[0], k.shape[0]
     qp, ql = _rows_of(q, n_q, p.n_heads, p, "q")
     kp, kl = _rows_of(k, n_k, p.n_kv_heads, p, "k")
     vp, vl = _rows_of(v, n_k, p.n_kv_heads, p, "v")
     wp, wb = _ws(workspace)
-    args = (qp, ql, n_q, kp, kl, vp, vl, n_k, _dense(cu_q, (n_seq + 1,), torch.int32, "cu_q"),
-            _dense(cu_k, (n_seq + 1,), torch.int32, "cu_k"), _dense(sinks, (p.n_heads,), torch.float32, "sinks"),
+    args = (qp, ql, n_q, kp, kl, vp, vl, n_k, _dense(cu_q, (n_seq + 1,), _dtype("i32"), "cu_q"),
+            _dense(cu_k, (n_seq + 1,), _dtype("i32"), "cu_k"), _dense(sinks, (p.n_heads,), _dtype(F32), "sinks"),
             _dense(out, (n_q, p.n_heads, p.head_dim), _act_dtype(p), "out"), wp, wb)
-    with _On(q, k, v, cu_q, cu_k, sinks, out, workspace):
-        _ok("prompt_attn", lib().prompt_attn(C.byref(p), n_seq, *args, _s(stream)))
+    _launch("prompt_attn", p, n_seq, args, stream, q, k, v, cu_q, cu_k, sinks, out, workspace)

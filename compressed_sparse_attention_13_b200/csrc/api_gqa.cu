@@ -45,10 +45,9 @@ extern "C" {
 size_t csa_gqa_workspace_size(const csa_gqa_params* p, int32_t op, int32_t n_seq, int64_t n_tokens, int64_t n_ctx) {
     if (op != CSA_OP_PAGED_DECODE && op != CSA_OP_PROMPT_ATTN) return 0;
     if (check_gqa(p, op == CSA_OP_PAGED_DECODE) || n_seq < 0 || n_tokens < 0 || n_ctx < 0) return 0;
-    if (op == CSA_OP_PAGED_DECODE && paged_decode_tc_supported(p->act_fmt, p->cache_fmt))
-        return paged_decode_workspace(p->n_heads, p->n_kv_heads, p->head_dim, n_seq, n_ctx,
-                                      (p->flags & CSA_FLAG_BATCH_INVARIANT) != 0);
-    return 256;
+    if (op == CSA_OP_PROMPT_ATTN) return 256;
+    return (paged_decode_tc_supported(p->act_fmt, p->cache_fmt) ? paged_decode_workspace : paged_decode_simt_workspace)(
+        p->n_heads, p->n_kv_heads, p->head_dim, n_seq, n_ctx, (p->flags & CSA_FLAG_BATCH_INVARIANT) != 0);
 }
 
 int paged_append(const csa_gqa_params* p, int32_t n_seq, int64_t n_tokens, const int32_t* cu_q,
@@ -112,7 +111,7 @@ int paged_decode_attn(const csa_gqa_params* p, int32_t batch, const void* q, int
     a.block_table = block_table; a.q_pos = q_pos; a.sinks = sinks; a.out = out;
     return cuda_status(paged_decode_tc_supported(p->act_fmt, p->cache_fmt)
                            ? launch_paged_decode_tc(a, workspace, (cudaStream_t)stream)
-                           : launch_paged_decode_simt(a, (cudaStream_t)stream));
+                           : launch_paged_decode_simt(a, workspace, (cudaStream_t)stream));
 }
 
 int prompt_attn(const csa_gqa_params* p, int32_t n_seq, const void* q, int64_t q_ld, int64_t n_q,

@@ -13,20 +13,10 @@
 //   S^T[token][head] = K . Q^T       A = K rows (ldmatrix), B = Q (registers)
 //   O^T[dim][head]  += V^T . P^T     A = V^T (ldmatrix.trans), B = P (movmatrix of S^T's layout)
 //
-// Work is dealt in steps of 64 visible tokens of one (sequence, head group):
-// the steps of all units are laid end to end and cut into equal ranges, one
-// per CTA (persistent, a multiple of the SMs), so ragged batches stay
-// balanced whatever their lengths, which only the device knows.  A unit that
-// lies in one CTA's range is written at once; the parts of others go to the
-// workspace as (m, l, O) and a small kernel joins them in order.  In batch
-// invariant mode a unit is cut at multiples of its own piece length instead
-// and the CTAs take whole pieces.
-//
-// In a CTA each of the four warps takes every fourth 16-token tile with its
-// own ring of cp.async stages (no CTA barrier in the loop); the ring runs on
-// across units.  The running maximum of a head is raised only when a tile
-// exceeds it by more than 8 in log2 units (one vote a tile otherwise), sums
-// stay per lane until the unit ends.
+// The split over the blocks and the copies: paged_split.cuh.  A warp's tile is
+// 16 tokens.  The running maximum of a head is raised only when a tile exceeds
+// it by more than 8 in log2 units (one vote a tile otherwise), sums stay per
+// lane until the unit ends.
 //
 // FP8 entries (E4M3 codes, fp32 scale per 64 channels) are converted to f16
 // exactly, one instruction per pair, and the MMAs run in f16: the query is
@@ -35,22 +25,19 @@
 // scales.  So that p * scale fits f16 whatever the scales, it is kept
 // relative to a power of two per (head, 64 channels) that follows its running
 // maximum, and O is in those units.
-#include "kernels.h"
+#include "paged_split.cuh"
 
 namespace csa {
 
 namespace {
 
-constexpr int kNW = 4;                 // warps of a CTA
-constexpr int kTok = 16;               // tokens of a warp's tile
-constexpr int kStep = kNW * kTok;      // tokens of a step
-constexpr int kMinSteps = 2;           // a CTA's share is not cut finer than this
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescale = 8.0f;       // log2 units
-constexpr uint32_t kNoRow = 0xFFFFFFFFu;
 
 template <int D, bool FP8, int NT>
 struct Dec {
+    static constexpr int kTok = 16;                      // tokens of a warp's tile
+    static constexpr int kStep = kNW * kTok;             // of a step
     static constexpr int kRow = FP8 ? D : 2 * D;         // bytes of a cache row
     static constexpr int kChunks = kRow / 16;
     static constexpr int kGroups = D / 64;
@@ -68,24 +55,6 @@ struct Dec {
     static constexpr int kSlot = kHeads * (D + 2);       // floats of a partial: (m, l) per head, O
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t smem_addr(const void* p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-template <int N>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, uint32_t n) {
-    if constexpr (N == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n), "n"(N) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
@@ -125,111 +94,7 @@ __device__ __forceinline__ void f16_of_e4m3(uint32_t w, uint32_t& lo, uint32_t& 
     asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
         : "=r"(lo), "=r"(hi) : "r"(w));
 }
-// Place of 16-byte chunk c of row r: ldmatrix reads eight rows' chunks without
-// bank conflicts (rows of 128 n bytes: by the row; of 64 or 192: by pairs).
-template <int CHUNKS>
-__device__ __forceinline__ uint32_t place(uint32_t r, uint32_t c) {
-    const uint32_t x = (CHUNKS & 7) == 0 ? (r & 7u) : ((r >> 1) & 3u);
-    return (r * CHUNKS + (c ^ x)) * 16u;
-}
-
-// Visible tokens [lo, lo + n) of a sequence and its steps and pieces.
-struct Span {
-    int64_t lo;
-    int n, steps;
-};
-
-__device__ __forceinline__ Span span_of(const PagedDecodeArgs& a, int64_t s) {
-    const int64_t t = a.q_pos[s], cap = a.max_pages * a.page_size;
-    Span v;
-    v.lo = a.W > 0 ? max(t - a.W + 1, int64_t(0)) : 0;
-    const int64_t hi = min(t + 1, cap);
-    v.n = int(max(hi - v.lo, int64_t(0)));
-    v.steps = max((v.n + kStep - 1) / kStep, 1);
-    return v;
-}
-
-// Batch invariant mode: steps of a piece, from the row's own length (at least
-// 512 tokens, at most 64 pieces).
-__host__ __device__ __forceinline__ int piece_steps(int steps) {
-    const int p = (steps + 63) / 64;
-    return p < 8 ? 8 : p;
-}
-
 }  // namespace
-
-// One CTA's share: units [.., x1) from position x (steps, or pieces).
-struct Cursor {
-    int64_t x, x1;
-    int s, u;          // sequence, unit within it
-    int at;            // position within the unit (steps or pieces)
-    Span v;
-};
-
-struct Plan {
-    int64_t x0, x1;    // this CTA's range
-    int s, u, at;      // where x0 lies
-    int n_ctas;        // CTAs that have a share
-    int64_t total;
-};
-
-__device__ __forceinline__ int weight(const PagedDecodeArgs& a, const Span& v) {
-    if (!a.invariant) return v.steps;
-    const int p = piece_steps(v.steps);
-    return (v.steps + p - 1) / p;
-}
-
-// Every CTA derives the same plan: threads sum the weights of consecutive
-// sequences, a scan gives their prefix, and the thread whose sequences hold
-// x0 walks to it.
-__device__ __forceinline__ void make_plan(const PagedDecodeArgs& a, int units, Plan* out) {
-    __shared__ int64_t warp_sum_[kNW];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t seg = (a.batch + 32 * kNW - 1) / (32 * kNW);
-    const int64_t s0 = min(tid * seg, a.batch), s1 = min(s0 + seg, a.batch);
-    int64_t mine = 0;
-    for (int64_t s = s0; s < s1; ++s) mine += int64_t(weight(a, span_of(a, s))) * units;
-    int64_t upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += y;
-    }
-    if (lane == 31) warp_sum_[warp] = upto;
-    __syncthreads();
-    int64_t total = 0;
-#pragma unroll
-    for (int w = 0; w < kNW; ++w) {
-        if (w < warp) upto += warp_sum_[w];
-        total += warp_sum_[w];
-    }
-    const int64_t least = a.invariant ? 1 : kMinSteps;
-    const int64_t n = min(int64_t(gridDim.x), (total + least - 1) / least);
-    const int64_t c = blockIdx.x;
-    const int64_t x0 = c < n ? c * total / n : total, x1 = c < n ? (c + 1) * total / n : total;
-    if (tid == 0) { out->x0 = x0; out->x1 = x1; out->n_ctas = int(n); out->total = total; }
-    int64_t x = upto - mine;  // prefix of this thread's first sequence
-    if (x0 < x1 && x0 >= x && x0 < upto) {
-        for (int64_t s = s0; s < s1; ++s) {
-            const int w = weight(a, span_of(a, s));
-            const int64_t e = x + int64_t(w) * units;
-            if (x0 < e) {
-                out->s = int(s);
-                out->u = int((x0 - x) / w);
-                out->at = int((x0 - x) % w);
-                break;
-            }
-            x = e;
-        }
-    }
-    __syncthreads();
-}
-
-// A record of the join: `n` parts, the first in slot `first`, the others in
-// slots next, next + by, ...; (s, u): the row they belong to.
-struct JoinRec {
-    int n, first, next, by, s, u, pad0, pad1;
-};
 
 template <int D, bool FP8, int NT>
 __global__ void __launch_bounds__(32 * kNW, Dec<D, FP8, NT>::kCtas)
@@ -243,110 +108,30 @@ __global__ void __launch_bounds__(32 * kNW, Dec<D, FP8, NT>::kCtas)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c4 = lane & 3;
     pdl_launch_dependents();
-    make_plan(a, units, &plan);
+    make_plan<C::kStep>(a, units, &plan);
     if (!a.invariant && threadIdx.x == 0) recs[blockIdx.x].n = 0;
     const int64_t x0 = plan.x0, x1 = plan.x1;
     if (x0 >= x1) return;
     const int G = a.H / a.HK;
     const float sl2 = a.scale * kLog2e;
 
-    // What remains of the unit at a cursor: steps [b, e), and how far x moves.
-    auto piece = [&](const Cursor& q, int& b, int& e, int& dx) {
-        if (a.invariant) {
-            const int p = piece_steps(q.v.steps);
-            b = q.at * p;
-            e = min(b + p, q.v.steps);
-            dx = 1;
-        } else {
-            b = q.at;
-            e = int(min(int64_t(q.v.steps), q.at + (q.x1 - q.x)));
-            dx = e - b;
-        }
-    };
-    auto advance = [&](Cursor& q, int dx) {
-        q.x += dx;
-        q.at += dx;
-        if (q.at >= weight(a, q.v)) {
-            q.at = 0;
-            if (++q.u == units) {
-                q.u = 0;
-                ++q.s;
-                if (q.x < q.x1) q.v = span_of(a, q.s);
-            }
-        }
-    };
-
     Cursor cur;
     cur.x = x0; cur.x1 = x1; cur.s = plan.s; cur.u = plan.u; cur.at = plan.at;
-    cur.v = span_of(a, cur.s);
+    cur.v = span_of<C::kStep>(a, cur.s);
 
     // ------------------------------------------------------- the copying side
-    Cursor pre = cur;
-    int pb, pe, pdx;
-    piece(pre, pb, pe, pdx);
+    constexpr int kTok = C::kTok;
     const uint32_t ring = smem_addr(smem) + uint32_t(warp) * C::kStages * C::kTile;
-    uint32_t row_next = kNoRow;
-    auto lookup = [&]() {  // cache row of token lane & 15 of the next tile to copy
-        row_next = kNoRow;
-        if (pre.x >= pre.x1) return;
-        const int tok = pb * kStep + warp * kTok + (lane & 15);
-        if (tok < pre.v.n) {
-            const int64_t i = pre.v.lo + tok;
-            const uint32_t pg = uint32_t(i) / uint32_t(a.page_size), off = uint32_t(i) % uint32_t(a.page_size);
-            const int64_t id = a.block_table[int64_t(pre.s) * a.max_pages + pg];
-            if (id >= 0 && id < a.n_pages)
-                row_next = (uint32_t(id) * uint32_t(a.HK) + uint32_t(pre.u / hb)) * uint32_t(a.page_size) + off;
-            else
-                flag_status(CSA_DEV_BAD_INDEX);
-        }
-    };
-    auto issue = [&](int stage) {  // copy the tile at `pre`, then look up the one after it
-        if (pre.x < pre.x1) {
-            const uint32_t k0 = ring + uint32_t(stage) * C::kTile, v0 = k0 + kTok * C::kRow;
-            const uint32_t row = row_next;
-            const unsigned ok = __ballot_sync(0xffffffffu, row != kNoRow) & 0xFFFFu;
-            if (lane == 0) vmask[warp][stage] = ok;
-#pragma unroll
-            for (int it = 0; it < kTok * C::kChunks / 32; ++it) {
-                const uint32_t i = uint32_t(it) * 32u + uint32_t(lane);
-                const uint32_t r = i / C::kChunks, ch = i % C::kChunks;
-                const uint32_t rr = __shfl_sync(0xffffffffu, row, int(r));
-                const uint32_t n = rr == kNoRow ? 0u : 16u;
-                const uint64_t off = rr == kNoRow ? 0ull : uint64_t(rr) * C::kRow + 16u * ch;
-                const uint32_t at = place<C::kChunks>(r, ch);
-                cp_async<16>(k0 + at, (const uint8_t*)a.k_cache + off, n);
-                cp_async<16>(v0 + at, (const uint8_t*)a.v_cache + off, n);
-            }
-            if constexpr (FP8) {  // lanes 0-15: key scales of their token, 16-31: value scales
-                const uint32_t s0 = v0 + kTok * C::kRow + (lane < 16 ? 0u : uint32_t(C::kScaleBytes));
-                const float* src = (lane < 16 ? a.k_scales : a.v_scales) + (row == kNoRow ? 0ull : uint64_t(row) * C::kGroups);
-                const uint32_t dst = s0 + uint32_t(lane & 15) * C::kGroups * 4;
-                const bool has = row != kNoRow;
-                if constexpr (C::kGroups == 3) {
-#pragma unroll
-                    for (int i = 0; i < 3; ++i) cp_async<4>(dst + 4 * i, src + i, has ? 4u : 0u);
-                } else {
-                    cp_async<C::kGroups * 4>(dst, src, has ? C::kGroups * 4u : 0u);
-                }
-            }
-            if (++pb >= pe) {
-                advance(pre, pdx);
-                if (pre.x < pre.x1) piece(pre, pb, pe, pdx);
-            }
-            lookup();
-        }
-        cp_commit();
-    };
-    lookup();
+    Copier<C, FP8> copier(a, units, hb, cur, ring, vmask[warp]);
 #pragma unroll 1
-    for (int i = 0; i < C::kStages - 1; ++i) issue(i);
+    for (int i = 0; i < C::kStages - 1; ++i) copier.issue(i);
 
     // ------------------------------------------------------ the computing side
     int stage = 0;
 #pragma unroll 1
     while (cur.x < cur.x1) {
         int b, e, dx;
-        piece(cur, b, e, dx);
+        piece_of<C::kStep>(a, cur, b, e, dx);
         if (threadIdx.x == 0 && a.q_pos[cur.s] >= a.max_pages * a.page_size) flag_status(CSA_DEV_BAD_INDEX);
         const int hk = cur.u / hb, head0 = (cur.u % hb) * C::kHeads;  // within the group of G
         const int n_heads = min(C::kHeads, G - head0);
@@ -415,7 +200,7 @@ __global__ void __launch_bounds__(32 * kNW, Dec<D, FP8, NT>::kCtas)
             __syncwarp();
             {
                 const int nx = stage == 0 ? C::kStages - 1 : stage - 1;  // the stage consumed last
-                issue(nx);
+                copier.issue(nx);
             }
             const uint32_t k0 = ring + uint32_t(stage) * C::kTile, v0 = k0 + kTok * C::kRow;
             const uint32_t ok = vmask[warp][stage];
@@ -610,31 +395,7 @@ __global__ void __launch_bounds__(32 * kNW, Dec<D, FP8, NT>::kCtas)
                 if (g == 0) jml[warp][8 * nt + 2 * c4 + i] = make_float2(m[nt][i], l[nt][i]);
             }
         const bool whole = b == 0 && e == cur.v.steps;
-        const bool first_unit = cur.x == x0;
-        int64_t slot = 0;
-        if (!whole) {
-            if (a.invariant) {
-                slot = cur.x;
-            } else {
-                slot = 2 * int64_t(blockIdx.x) + (first_unit ? 0 : 1);
-                // the CTA that holds the unit's beginning says where its parts are
-                if (b == 0 && threadIdx.x == 0) {
-                    // the last CTA with a part of it: that of the unit's last step
-                    const int64_t xe = cur.x + cur.v.steps - 1;
-                    const int64_t last = ((xe + 1) * plan.n_ctas + plan.total - 1) / plan.total - 1;
-                    JoinRec r;
-                    r.n = int(last - blockIdx.x) + 1; r.first = int(slot); r.next = 2 * (blockIdx.x + 1); r.by = 2;
-                    r.s = cur.s; r.u = cur.u; r.pad0 = r.pad1 = 0;
-                    recs[blockIdx.x] = r;
-                }
-            }
-        }
-        if (a.invariant && b == 0 && threadIdx.x == 0) {
-            JoinRec r;
-            r.n = whole ? 0 : weight(a, cur.v); r.first = int(slot); r.next = int(slot) + 1; r.by = 1;
-            r.s = cur.s; r.u = cur.u; r.pad0 = r.pad1 = 0;
-            recs[int64_t(cur.s) * units + cur.u] = r;
-        }
+        const int64_t slot = part_slot(a, plan, cur, units, weight<C::kStep>(a, cur.v), b == 0, whole, recs);
 #pragma unroll
         for (int pass = 0; pass < NT * D / C::kJoinDims; ++pass) {
             const int nt = pass % NT, k0 = pass / NT * (C::kJoinDims / 16);
@@ -677,7 +438,7 @@ __global__ void __launch_bounds__(32 * kNW, Dec<D, FP8, NT>::kCtas)
             }
             __syncthreads();
         }
-        advance(cur, dx);
+        advance<C::kStep>(a, units, cur, dx);
     }
     cp_wait<0>();
 }
@@ -707,7 +468,10 @@ __global__ void __launch_bounds__(128)
             L += wt * lq;
             if (wt != 0.f) acc += wt * x;
         }
-        ((__nv_bfloat16*)a.out)[(int64_t(r.s) * a.H + h) * D + i % D] = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L);
+        const int64_t at = (int64_t(r.s) * a.H + h) * D + i % D;
+        const float y = L == 0.f ? 0.f : acc / L;
+        if (a.act_fmt == CSA_F32) ((float*)a.out)[at] = y;
+        else ((__nv_bfloat16*)a.out)[at] = __float2bfloat16_rn(y);
     }
 }
 
@@ -718,20 +482,13 @@ bool paged_decode_tc_supported(int act, int cache) {
     return act == CSA_BF16 && (cache == CSA_BF16 || cache == CSA_FP8_S64);
 }
 
-struct DecodeLayout {
-    int64_t units, recs;   // per sequence; records
-    int64_t slots;
-    size_t rec_bytes, bytes;
-};
-
-static DecodeLayout decode_layout(int H, int HK, int D, int64_t batch, int64_t n_ctx, bool invariant) {
-    const int heads = group_heads(H, HK, D);
+DecodeLayout decode_layout(int H, int HK, int D, int64_t batch, int64_t n_ctx, bool invariant, int heads, int step) {
     DecodeLayout w;
     w.units = int64_t(HK) * ((H / HK + heads - 1) / heads);
     if (invariant) {
-        const int64_t steps = ceil_div(n_ctx, kStep);
+        const int64_t steps = ceil_div(n_ctx, step);
         w.recs = batch * w.units;
-        w.slots = batch * w.units * std::min<int64_t>(64, ceil_div(steps, 8) + 1);
+        w.slots = batch * w.units * std::min<int64_t>(64, ceil_div(steps, 512 / step) + 1);
     } else {
         w.recs = 2 * kNumSMs;
         w.slots = 2 * w.recs;
@@ -741,15 +498,24 @@ static DecodeLayout decode_layout(int H, int HK, int D, int64_t batch, int64_t n
     return w;
 }
 
+cudaError_t launch_paged_join(const PagedDecodeArgs& a, int64_t recs_n, int hb, int heads, const JoinRec* recs,
+                              const float* slots, cudaStream_t s) {
+    return launch_ex(paged_decode_join_kernel, dim3(unsigned(recs_n), 2), dim3(128), 0, s, true, a, hb, heads, recs,
+                     slots);
+}
+
+constexpr int kStepTc = 64;
+
 size_t paged_decode_workspace(int H, int HK, int D, int64_t batch, int64_t n_ctx, bool invariant) {
-    return decode_layout(H, HK, D, batch, n_ctx, invariant).bytes;
+    return decode_layout(H, HK, D, batch, n_ctx, invariant, group_heads(H, HK, D), kStepTc).bytes;
 }
 
 template <int D, bool FP8, int NT>
 static cudaError_t launch_decode(const PagedDecodeArgs& a, void* ws, cudaStream_t s) {
     using C = Dec<D, FP8, NT>;
     static_assert(C::kStages >= 2 && C::kStages <= 8, "stages");
-    const DecodeLayout w = decode_layout(a.H, a.HK, D, a.batch, a.max_pages * a.page_size, a.invariant);
+    static_assert(C::kStep == kStepTc, "steps");
+    const DecodeLayout w = decode_layout(a.H, a.HK, D, a.batch, a.max_pages * a.page_size, a.invariant, C::kHeads, C::kStep);
     JoinRec* recs = (JoinRec*)ws;
     float* slots = (float*)((char*)ws + w.rec_bytes);
     const int hb = int(w.units / a.HK);
@@ -758,9 +524,7 @@ static cudaError_t launch_decode(const PagedDecodeArgs& a, void* ws, cudaStream_
     paged_decode_kernel<D, FP8, NT><<<C::kCtas * kNumSMs, 32 * kNW, C::kSmem, s>>>(a, int(w.units), hb, recs, slots);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const unsigned n = unsigned(a.invariant ? w.recs : C::kCtas * kNumSMs);
-    return launch_ex(paged_decode_join_kernel, dim3(n, 2), dim3(128), 0, s, true, a, hb, int(C::kHeads),
-                     (const JoinRec*)recs, (const float*)slots);
+    return launch_paged_join(a, a.invariant ? w.recs : C::kCtas * kNumSMs, hb, C::kHeads, recs, slots, s);
 }
 
 template <int D, bool FP8>

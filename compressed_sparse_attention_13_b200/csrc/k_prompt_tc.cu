@@ -44,6 +44,7 @@
 // moves registers from the other warps to the softmax.
 #include <string.h>
 
+#include "gqa_tiles.cuh"
 #include "kernels.h"
 #include "sm100.cuh"
 #include "tmap.h"
@@ -151,34 +152,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 }  // namespace
-
-// The tile of a packed batch: sequences in order, the tiles of a sequence last
-// (longest) first.  Called by one warp; s = -1 behind the last tile.
-__device__ __forceinline__ void find_tile(const int32_t* cu, int n_seq, int per, int x, int lane, int& s, int& tile) {
-    int before = 0;
-    s = -1;
-    tile = 0;
-    for (int base = 0; base < n_seq; base += 32) {
-        const int i = base + lane;
-        const int n = i < n_seq ? max(cu[i + 1] - cu[i], 0) : 0;
-        const int mine = (n + per - 1) / per;
-        int upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += y;
-        }
-        const unsigned in = __ballot_sync(0xffffffffu, x < before + upto);
-        if (in) {
-            const int src = __ffs(int(in)) - 1;
-            s = base + src;
-            const int end = before + __shfl_sync(0xffffffffu, upto, src);
-            tile = end - 1 - x;  // counted from the sequence's last tile
-            return;
-        }
-        before += __shfl_sync(0xffffffffu, upto, 31);
-    }
-}
 
 template <int D>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)

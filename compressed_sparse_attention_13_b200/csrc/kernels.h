@@ -133,7 +133,8 @@ struct PagedDecodeArgs {
     const float* sinks;          // [H] or null
     void* out;                   // [batch][H][D]
 };
-cudaError_t launch_paged_decode_simt(const PagedDecodeArgs& a, cudaStream_t s);
+size_t paged_decode_simt_workspace(int H, int HK, int D, int64_t batch, int64_t n_ctx, bool invariant);
+cudaError_t launch_paged_decode_simt(const PagedDecodeArgs& a, void* ws, cudaStream_t s);
 bool paged_decode_tc_supported(int act, int cache);
 size_t paged_decode_workspace(int H, int HK, int D, int64_t batch, int64_t n_ctx, bool invariant);
 cudaError_t launch_paged_decode_tc(const PagedDecodeArgs& a, void* ws, cudaStream_t s);
