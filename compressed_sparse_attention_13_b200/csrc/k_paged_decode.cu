@@ -443,35 +443,72 @@ __global__ void __launch_bounds__(32 * kNW, Dec<D, FP8, NT>::kCtas)
     cp_wait<0>();
 }
 
-// Join the parts of the rows that more than one CTA (or piece) worked on.
-__global__ void __launch_bounds__(128)
+// Join the parts of the rows that more than one block (or piece) worked on.  A
+// block joins a quarter of a unit's heads * D outputs: its warps first turn the
+// parts' maxima and sums into weights (a warp per head), then its threads take
+// four dims each and the parts in groups, added in the groups' order.
+constexpr int kJoinThreads = 256, kJoinParts = 2 * kNumSMs;
+
+__global__ void __launch_bounds__(kJoinThreads)
     paged_decode_join_kernel(const PagedDecodeArgs a, int hb, int heads, const JoinRec* recs, const float* slots) {
+    __shared__ float wt[16 * kJoinParts / 4 + 2 * kJoinParts], inv[16];
+    __shared__ float4 part[kJoinThreads];
     pdl_wait();
     const JoinRec r = recs[blockIdx.x];
     if (r.n == 0) return;
-    const int D = a.D, G = a.H / a.HK, per = heads * (D + 2);
+    const int D = a.D, G = a.H / a.HK, per = heads * (D + 2), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int hk = r.u / hb, head0 = (r.u % hb) * heads, n_heads = min(heads, G - head0);
-    for (int i = threadIdx.x + 128 * blockIdx.y; i < n_heads * D; i += 128 * gridDim.y) {
-        const int head = i / D, h = hk * G + head0 + head;
-        const float sg = a.sinks ? a.sinks[h] * kLog2e : -INFINITY;
-        float M = sg;
-        for (int q = 0; q < r.n; ++q) {
-            const float* sp = slots + int64_t(q == 0 ? r.first : r.next + (q - 1) * r.by) * per;
-            M = fmaxf(M, sp[2 * head]);
+    const int share = heads * D / 16, i0 = blockIdx.y * share;  // in groups of four dims
+    const int h0 = i0 * 4 / D, h1 = min((i0 + share) * 4 / D + (share * 4 % D != 0), n_heads);  // heads of the share
+    auto slot = [&](int q) { return slots + int64_t(q == 0 ? r.first : r.next + (q - 1) * r.by) * per; };
+    for (int h = h0 + warp; h < h1; h += kJoinThreads / 32) {
+        const float sg = a.sinks ? a.sinks[hk * G + head0 + h] * kLog2e : -INFINITY;
+        float M = sg, L = 0.f;
+        for (int q = lane; q < r.n; q += 32) M = fmaxf(M, slot(q)[2 * h]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        for (int q = lane; q < r.n; q += 32) {
+            const float2 ml = *reinterpret_cast<const float2*>(slot(q) + 2 * h);
+            const float x = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+            L += x * ml.y;  // (NaN stays NaN)
+            wt[(h - h0) * r.n + q] = x;
         }
-        float L = sg != -INFINITY ? ex2(sg - M) : 0.f, acc = 0.f;
+        L = warp_sum(L);
+        if (sg != -INFINITY) L += ex2(sg - M);
+        if (lane == 0) inv[h - h0] = L;
+    }
+    __syncthreads();
+    const int groups = kJoinThreads / share, g = threadIdx.x / share, i = i0 + threadIdx.x % share;
+    const int h = i * 4 / D;
+    const bool on = g < groups && h < n_heads;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (on) {
+        const float* w = wt + (h - h0) * r.n;
 #pragma unroll 4
-        for (int q = 0; q < r.n; ++q) {
-            const float* sp = slots + int64_t(q == 0 ? r.first : r.next + (q - 1) * r.by) * per;
-            const float mq = sp[2 * head], lq = sp[2 * head + 1], x = sp[2 * heads + i];
-            const float wt = mq == -INFINITY ? 0.f : ex2(mq - M);
-            L += wt * lq;
-            if (wt != 0.f) acc += wt * x;
+        for (int q = g; q < r.n; q += groups) {
+            const float2* p = reinterpret_cast<const float2*>(slot(q) + 2 * heads + 4 * i);
+            const float2 x = p[0], y = p[1];
+            if (w[q] != 0.f) {
+                acc.x += w[q] * x.x; acc.y += w[q] * x.y;
+                acc.z += w[q] * y.x; acc.w += w[q] * y.y;
+            }
         }
-        const int64_t at = (int64_t(r.s) * a.H + h) * D + i % D;
-        const float y = L == 0.f ? 0.f : acc / L;
-        if (a.act_fmt == CSA_F32) ((float*)a.out)[at] = y;
-        else ((__nv_bfloat16*)a.out)[at] = __float2bfloat16_rn(y);
+    }
+    part[threadIdx.x] = acc;
+    __syncthreads();
+    if (!on || g != 0) return;
+    for (int k = 1; k < groups; ++k) {
+        const float4 x = part[threadIdx.x + k * share];
+        acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+    }
+    const float L = inv[h - h0];
+    const float y[4] = {acc.x / L, acc.y / L, acc.z / L, acc.w / L};
+    const int64_t at = (int64_t(r.s) * a.H + hk * G + head0) * D + 4 * i;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float z = L == 0.f ? 0.f : y[k];
+        if (a.act_fmt == CSA_F32) ((float*)a.out)[at + k] = z;
+        else ((__nv_bfloat16*)a.out)[at + k] = __float2bfloat16_rn(z);
     }
 }
 
@@ -480,6 +517,13 @@ static int group_heads(int H, int HK, int D) { return H / HK > 8 && D <= 128 ? 1
 
 bool paged_decode_tc_supported(int act, int cache) {
     return act == CSA_BF16 && (cache == CSA_BF16 || cache == CSA_FP8_S64);
+}
+
+void set_page_division(PagedDecodeArgs* a) {
+    int s = 0;
+    while ((int64_t(1) << s) < a->page_size) ++s;
+    a->page_mul = s ? uint32_t(((uint64_t(1) << (31 + s)) + a->page_size - 1) / a->page_size) : 0;
+    a->page_shift = s ? s - 1 : 0;
 }
 
 DecodeLayout decode_layout(int H, int HK, int D, int64_t batch, int64_t n_ctx, bool invariant, int heads, int step) {
@@ -500,7 +544,7 @@ DecodeLayout decode_layout(int H, int HK, int D, int64_t batch, int64_t n_ctx, b
 
 cudaError_t launch_paged_join(const PagedDecodeArgs& a, int64_t recs_n, int hb, int heads, const JoinRec* recs,
                               const float* slots, cudaStream_t s) {
-    return launch_ex(paged_decode_join_kernel, dim3(unsigned(recs_n), 2), dim3(128), 0, s, true, a, hb, heads, recs,
+    return launch_ex(paged_decode_join_kernel, dim3(unsigned(recs_n), 4), dim3(kJoinThreads), 0, s, true, a, hb, heads, recs,
                      slots);
 }
 
@@ -544,7 +588,9 @@ static cudaError_t launch_decode_fmt(const PagedDecodeArgs& a, void* ws, cudaStr
     }
 }
 
-cudaError_t launch_paged_decode_tc(const PagedDecodeArgs& a, void* ws, cudaStream_t s) {
+cudaError_t launch_paged_decode_tc(const PagedDecodeArgs& args, void* ws, cudaStream_t s) {
+    PagedDecodeArgs a = args;
+    set_page_division(&a);
     return a.cache_fmt == CSA_FP8_S64 ? launch_decode_fmt<true>(a, ws, s) : launch_decode_fmt<false>(a, ws, s);
 }
 

@@ -320,7 +320,9 @@ static cudaError_t launch_fmt(const PagedDecodeArgs& a, void* ws, cudaStream_t s
     }
 }
 
-cudaError_t launch_paged_decode_simt(const PagedDecodeArgs& a, void* ws, cudaStream_t s) {
+cudaError_t launch_paged_decode_simt(const PagedDecodeArgs& args, void* ws, cudaStream_t s) {
+    PagedDecodeArgs a = args;
+    set_page_division(&a);
     if (a.cache_fmt == CSA_F32) return launch_fmt<CSA_F32>(a, ws, s);
     if (a.cache_fmt == CSA_BF16) return launch_fmt<CSA_BF16>(a, ws, s);
     return launch_fmt<CSA_FP8_S64>(a, ws, s);

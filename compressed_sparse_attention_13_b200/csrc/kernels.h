@@ -132,6 +132,7 @@ struct PagedDecodeArgs {
     const int64_t* q_pos;        // [batch]
     const float* sinks;          // [H] or null
     void* out;                   // [batch][H][D]
+    uint32_t page_mul, page_shift;  // division by page_size (set by the launcher)
 };
 size_t paged_decode_simt_workspace(int H, int HK, int D, int64_t batch, int64_t n_ctx, bool invariant);
 cudaError_t launch_paged_decode_simt(const PagedDecodeArgs& a, void* ws, cudaStream_t s);

@@ -187,7 +187,12 @@ struct Copier {
     int units, hb;
     Cursor pre;
     int pb, pe, pdx;
-    uint32_t ring, row_next;
+    uint32_t ring;
+    // Of token lane % kTok of the next tile to copy: its page's entry of the block
+    // table (loaded a tile ahead and first looked at when the tile is copied: its
+    // latency is not waited for), place in the page, and key head; off < 0: no token.
+    int32_t id;
+    int off, hk;
     uint32_t* vmask;
 
     __device__ __forceinline__ Copier(const PagedDecodeArgs& a_, int units_, int hb_, const Cursor& c, uint32_t ring_,
@@ -196,26 +201,31 @@ struct Copier {
         piece_of<C::kStep>(a, pre, pb, pe, pdx);
         lookup();
     }
-    __device__ __forceinline__ void lookup() {  // cache row of token lane % kTok of the next tile to copy
+    __device__ __forceinline__ void lookup() {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        row_next = kNoRow;
+        off = -1;
         if (pre.x >= pre.x1) return;
         const int tok = pb * C::kStep + warp * C::kTok + (lane & (C::kTok - 1));
         if (tok < pre.v.n) {
-            const int64_t i = pre.v.lo + tok;
-            const uint32_t pg = uint32_t(i) / uint32_t(a.page_size), off = uint32_t(i) % uint32_t(a.page_size);
-            const int64_t id = a.block_table[int64_t(pre.s) * a.max_pages + pg];
-            if (id >= 0 && id < a.n_pages)
-                row_next = (uint32_t(id) * uint32_t(a.HK) + uint32_t(pre.u / hb)) * uint32_t(a.page_size) + off;
-            else
-                flag_status(CSA_DEV_BAD_INDEX);
+            const uint32_t i = uint32_t(pre.v.lo) + uint32_t(tok);
+            const uint32_t pg = a.page_size == 1 ? i : __umulhi(i, a.page_mul) >> a.page_shift;
+            off = int(i - pg * uint32_t(a.page_size));
+            hk = pre.u / hb;
+            id = a.block_table[int64_t(pre.s) * a.max_pages + pg];
         }
+    }
+    __device__ __forceinline__ uint32_t resolve() {  // the token's cache row
+        if (off < 0) return kNoRow;
+        if (id >= 0 && id < a.n_pages)
+            return (uint32_t(id) * uint32_t(a.HK) + uint32_t(hk)) * uint32_t(a.page_size) + uint32_t(off);
+        flag_status(CSA_DEV_BAD_INDEX);
+        return kNoRow;
     }
     __device__ __forceinline__ void issue(int stage) {  // copy the tile at `pre`, then look up the one after it
         const int lane = threadIdx.x & 31;
         if (pre.x < pre.x1) {
             const uint32_t k0 = ring + uint32_t(stage) * C::kTile, v0 = k0 + C::kTok * C::kRow;
-            const uint32_t row = row_next;
+            const uint32_t row = resolve();
             const unsigned ok = __ballot_sync(0xffffffffu, row != kNoRow) & ((1u << C::kTok) - 1u);
             if (lane == 0) vmask[stage] = ok;
 #pragma unroll
@@ -287,6 +297,10 @@ struct DecodeLayout {
     int64_t units, recs, slots;
     size_t rec_bytes, bytes;
 };
+// Sets page_mul and page_shift: i / page_size for 0 <= i < 2^31 is the high word
+// of i * page_mul, shifted, with page_mul = 2^(31 + s) / page_size rounded up,
+// s = ceil(log2 page_size): off by less than i / 2^31 / page_size from the quotient.
+void set_page_division(PagedDecodeArgs* a);
 DecodeLayout decode_layout(int H, int HK, int D, int64_t batch, int64_t n_ctx, bool invariant, int heads, int step);
 cudaError_t launch_paged_join(const PagedDecodeArgs& a, int64_t recs_n, int hb, int heads, const JoinRec* recs,
                               const float* slots, cudaStream_t s);
