@@ -51,7 +51,7 @@ struct Dec {
     static constexpr int kJoin = kJoinDims + 4;          // padded row of the join buffer
     static constexpr int kRing = kNW * kStages * kTile;
     static constexpr int kSmem = kRing + kNW * 8 * kJoin * 4;
-    static constexpr int kCtas = 2 * (kSmem + 2048) <= 228 * 1024 ? 2 : 1;  // per SM
+    static constexpr int kCtas = 2 * (kSmem + 3072) <= 228 * 1024 ? 2 : 1;  // per SM
     static constexpr int kSlot = kHeads * (D + 2);       // floats of a partial: (m, l) per head, O
 };
 
@@ -100,7 +100,8 @@ template <int D, bool FP8, int NT>
 __global__ void __launch_bounds__(32 * kNW, Dec<D, FP8, NT>::kCtas)
     paged_decode_kernel(const PagedDecodeArgs a, int units, int hb, JoinRec* recs, float* slots) {
     using C = Dec<D, FP8, NT>;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* const smem = aligned_smem(smem_raw);
     __shared__ Plan plan;
     __shared__ uint32_t vmask[kNW][8];
     __shared__ float2 jml[kNW][8 * NT];
@@ -213,13 +214,22 @@ __global__ void __launch_bounds__(32 * kNW, Dec<D, FP8, NT>::kCtas)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
             if constexpr (!FP8) {
+                float s1[NT][4];  // a second chain of products: half the latency
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s1[nt][i] = 0.f;
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     uint32_t x[4];
-                    ldsm4(k0 + place<C::kChunks>(lane & 15, 2 * k + (lane >> 4)), x);
+                    ldsm4(k0 + place<kTok, C::kRow>(lane & 15, 2 * k + (lane >> 4)), x);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma<false>(s[nt], x, qf[nt][k][0], qf[nt][k][1]);
+                    for (int nt = 0; nt < NT; ++nt) mma<false>(k & 1 ? s1[nt] : s[nt], x, qf[nt][k][0], qf[nt][k][1]);
                 }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[nt][i] += s1[nt][i];
             } else {
 #pragma unroll
                 for (int gr = 0; gr < C::kGroups; ++gr) {
@@ -231,7 +241,7 @@ __global__ void __launch_bounds__(32 * kNW, Dec<D, FP8, NT>::kCtas)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {  // 32 dims
                         uint32_t w[4];
-                        ldsm4(k0 + place<C::kChunks>(lane & 15, 4 * gr + 2 * h + (lane >> 4)), w);
+                        ldsm4(k0 + place<kTok, C::kRow>(lane & 15, 4 * gr + 2 * h + (lane >> 4)), w);
 #pragma unroll
                         for (int z = 0; z < 2; ++z) {
                             uint32_t x[4];
@@ -322,7 +332,7 @@ __global__ void __launch_bounds__(32 * kNW, Dec<D, FP8, NT>::kCtas)
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     uint32_t x[4];
-                    ldsm4_t(v0 + place<C::kChunks>((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)), x);
+                    ldsm4_t(v0 + place<kTok, C::kRow>((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)), x);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) mma<false>(o[nt][k], x, p[nt][0], p[nt][1]);
                 }
@@ -368,7 +378,7 @@ __global__ void __launch_bounds__(32 * kNW, Dec<D, FP8, NT>::kCtas)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t w[4];
-                        ldsm4_t(v0 + place<C::kChunks>(lane & 15, 4 * gr + 2 * h + (lane >> 4)), w);
+                        ldsm4_t(v0 + place<kTok, C::kRow>(lane & 15, 4 * gr + 2 * h + (lane >> 4)), w);
 #pragma unroll
                         for (int z = 0; z < 2; ++z) {
                             // tokens 2 c4, 2 c4 + 1 of dims 2 g (low half) and 2 g + 1 (high half)
@@ -563,9 +573,9 @@ static cudaError_t launch_decode(const PagedDecodeArgs& a, void* ws, cudaStream_
     JoinRec* recs = (JoinRec*)ws;
     float* slots = (float*)((char*)ws + w.rec_bytes);
     const int hb = int(w.units / a.HK);
-    cudaError_t e = ensure_smem(paged_decode_kernel<D, FP8, NT>, C::kSmem);
+    cudaError_t e = ensure_smem(paged_decode_kernel<D, FP8, NT>, C::kSmem + kAlignSmem);
     if (e != cudaSuccess) return e;
-    paged_decode_kernel<D, FP8, NT><<<C::kCtas * kNumSMs, 32 * kNW, C::kSmem, s>>>(a, int(w.units), hb, recs, slots);
+    paged_decode_kernel<D, FP8, NT><<<C::kCtas * kNumSMs, 32 * kNW, C::kSmem + kAlignSmem, s>>>(a, int(w.units), hb, recs, slots);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_paged_join(a, a.invariant ? w.recs : C::kCtas * kNumSMs, hb, C::kHeads, recs, slots, s);

@@ -36,7 +36,7 @@ struct Dec {
     static constexpr int kRing = kNW * kStages * kTile;
     static constexpr int kJoinDims = D > 64 ? D / 2 : D;
     static constexpr int kSmem = kRing + (NH * D + kNW * NH * kJoinDims + kNW * kTok * NH) * 4;
-    static constexpr int kCtas = 2 * (kSmem + 2048) <= 228 * 1024 ? 2 : 1;  // per SM
+    static constexpr int kCtas = 2 * (kSmem + 3072) <= 228 * 1024 ? 2 : 1;  // per SM
 };
 
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
@@ -65,24 +65,24 @@ __device__ __forceinline__ uint64_t e4m3_pair(uint32_t w) {  // two codes, exact
 template <class C, int FMT>
 __device__ __forceinline__ void load4(const uint8_t* base, int r, int d, uint64_t (&x)[2]) {
     if constexpr (FMT == CSA_F32) {
-        const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(base + place<C::kChunks>(r, d / 4));
+        const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(base + place<C::kTok, C::kRow>(r, d / 4));
         x[0] = y.x;
         x[1] = y.y;
     } else if constexpr (FMT == CSA_BF16) {
-        const uint2 y = *reinterpret_cast<const uint2*>(base + place<C::kChunks>(r, d / 8) + d % 8 * 2);
+        const uint2 y = *reinterpret_cast<const uint2*>(base + place<C::kTok, C::kRow>(r, d / 8) + d % 8 * 2);
         x[0] = bf16_pair(y.x);
         x[1] = bf16_pair(y.y);
     } else {
-        const uint32_t y = *reinterpret_cast<const uint32_t*>(base + place<C::kChunks>(r, d / 16) + d % 16);
+        const uint32_t y = *reinterpret_cast<const uint32_t*>(base + place<C::kTok, C::kRow>(r, d / 16) + d % 16);
         x[0] = e4m3_pair(y);
         x[1] = e4m3_pair(y >> 16);
     }
 }
 template <class C, int FMT>
 __device__ __forceinline__ uint64_t load2(const uint8_t* base, int r, int d) {
-    if constexpr (FMT == CSA_F32) return *reinterpret_cast<const uint64_t*>(base + place<C::kChunks>(r, d / 4) + d % 4 * 4);
-    else if constexpr (FMT == CSA_BF16) return bf16_pair(*reinterpret_cast<const uint32_t*>(base + place<C::kChunks>(r, d / 8) + d % 8 * 2));
-    else return e4m3_pair(*reinterpret_cast<const uint16_t*>(base + place<C::kChunks>(r, d / 16) + d % 16));
+    if constexpr (FMT == CSA_F32) return *reinterpret_cast<const uint64_t*>(base + place<C::kTok, C::kRow>(r, d / 4) + d % 4 * 4);
+    else if constexpr (FMT == CSA_BF16) return bf16_pair(*reinterpret_cast<const uint32_t*>(base + place<C::kTok, C::kRow>(r, d / 8) + d % 8 * 2));
+    else return e4m3_pair(*reinterpret_cast<const uint16_t*>(base + place<C::kTok, C::kRow>(r, d / 16) + d % 16));
 }
 
 }  // namespace
@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(32 * kNW, Dec<D, FMT, NH>::kCtas)
     paged_decode_simt_kernel(const PagedDecodeArgs a, int units, int hb, JoinRec* recs, float* slots) {
     using C = Dec<D, FMT, NH>;
     constexpr int kTok = C::kTok, JD = C::kJoinDims;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* const smem = aligned_smem(smem_raw);
     __shared__ Plan plan;
     __shared__ uint32_t vmask[kNW][8];
     __shared__ float2 jml[kNW][NH];
@@ -296,14 +297,14 @@ size_t paged_decode_simt_workspace(int H, int HK, int D, int64_t batch, int64_t 
 template <int D, int FMT, int NH>
 static cudaError_t launch_nh(const PagedDecodeArgs& a, void* ws, cudaStream_t s) {
     using C = Dec<D, FMT, NH>;
-    static_assert(C::kStages >= 2 && C::kStages <= 8 && C::kStep == kStepSimt && C::kSmem <= 227 * 1024 - 2048, "tile");
+    static_assert(C::kStages >= 2 && C::kStages <= 8 && C::kStep == kStepSimt && C::kSmem <= 227 * 1024 - 3072, "tile");
     const DecodeLayout w = decode_layout(a.H, a.HK, D, a.batch, a.max_pages * a.page_size, a.invariant, NH, C::kStep);
     JoinRec* recs = (JoinRec*)ws;
     float* slots = (float*)((char*)ws + w.rec_bytes);
     const int hb = int(w.units / a.HK);
-    cudaError_t e = ensure_smem(paged_decode_simt_kernel<D, FMT, NH>, C::kSmem);
+    cudaError_t e = ensure_smem(paged_decode_simt_kernel<D, FMT, NH>, C::kSmem + kAlignSmem);
     if (e != cudaSuccess) return e;
-    paged_decode_simt_kernel<D, FMT, NH><<<C::kCtas * kNumSMs, 32 * kNW, C::kSmem, s>>>(a, int(w.units), hb, recs, slots);
+    paged_decode_simt_kernel<D, FMT, NH><<<C::kCtas * kNumSMs, 32 * kNW, C::kSmem + kAlignSmem, s>>>(a, int(w.units), hb, recs, slots);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_paged_join(a, a.invariant ? w.recs : C::kCtas * kNumSMs, hb, NH, recs, slots, s);

@@ -42,12 +42,26 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, uint32_t
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-// Place of 16-byte chunk c of row r: ldmatrix reads eight rows' chunks without
-// bank conflicts (rows of 128 n bytes: by the row; of 64 or 192: by pairs).
-template <int CHUNKS>
+// Shared memory for the rings, from a multiple of 128 bytes on: `extern
+// __shared__` alone does not give one behind static arrays, whatever its
+// declared alignment, and 16-byte copies of one 128-byte line into two shared
+// lines cross from L2 twice (131,072 keys: 337 us instead of 269).
+constexpr int kAlignSmem = 1024;
+__device__ __forceinline__ uint8_t* aligned_smem(uint8_t* p) {
+    return p + ((kAlignSmem - (smem_addr(p) & (kAlignSmem - 1))) & (kAlignSmem - 1));
+}
+
+// Place of 16-byte chunk c of row r in a tile of TOK rows of ROW bytes.  Rows are
+// cut into blocks of 128 bytes (64 where those do not divide them), each block's
+// rows one after another and swizzled, so that ldmatrix, and eight lanes on one
+// chunk of eight rows, hit all banks.  (Swizzled tensor copies, which need no place
+// computed, took longer: 276 us instead of 269 for 131,072 keys, and 274 instead
+// of 190 from FP8 pages, whose tiles are half as large.)
+template <int TOK, int ROW>
 __device__ __forceinline__ uint32_t place(uint32_t r, uint32_t c) {
-    const uint32_t x = (CHUNKS & 7) == 0 ? (r & 7u) : ((r >> 1) & 3u);
-    return (r * CHUNKS + (c ^ x)) * 16u;
+    constexpr uint32_t B = ROW % 128 == 0 ? 128 : 64, per = B / 16;
+    const uint32_t x = per == 8 ? (r & 7u) : ((r >> 1) & 3u);
+    return c / per * (TOK * B) + r * B + ((c % per) ^ x) * 16u;
 }
 
 // Visible tokens [lo, lo + n) of a sequence and its steps and pieces.
@@ -228,6 +242,19 @@ struct Copier {
             const uint32_t row = resolve();
             const unsigned ok = __ballot_sync(0xffffffffu, row != kNoRow) & ((1u << C::kTok) - 1u);
             if (lane == 0) vmask[stage] = ok;
+            // mostly the tile's rows follow one another in a page: then their bytes do, too
+            const uint32_t row0 = __shfl_sync(0xffffffffu, row, 0);
+            if (__all_sync(0xffffffffu, row == row0 + uint32_t(lane & (C::kTok - 1)) && row != kNoRow)) {
+                const uint64_t off0 = uint64_t(row0) * C::kRow + 16u * uint32_t(lane);
+                const uint8_t *ks = (const uint8_t*)a.k_cache + off0, *vs = (const uint8_t*)a.v_cache + off0;
+#pragma unroll
+                for (int it = 0; it < C::kTok * C::kChunks / 32; ++it) {
+                    const uint32_t i = uint32_t(it) * 32u + uint32_t(lane);
+                    const uint32_t at = place<C::kTok, C::kRow>(i / C::kChunks, i % C::kChunks);
+                    cp_async<16>(k0 + at, ks + 512 * it, 16u);
+                    cp_async<16>(v0 + at, vs + 512 * it, 16u);
+                }
+            } else
 #pragma unroll
             for (int it = 0; it < C::kTok * C::kChunks / 32; ++it) {
                 const uint32_t i = uint32_t(it) * 32u + uint32_t(lane);
@@ -235,7 +262,7 @@ struct Copier {
                 const uint32_t rr = __shfl_sync(0xffffffffu, row, int(r));
                 const uint32_t n = rr == kNoRow ? 0u : 16u;
                 const uint64_t off = rr == kNoRow ? 0ull : uint64_t(rr) * C::kRow + 16u * ch;
-                const uint32_t at = place<C::kChunks>(r, ch);
+                const uint32_t at = place<C::kTok, C::kRow>(r, ch);
                 cp_async<16>(k0 + at, (const uint8_t*)a.k_cache + off, n);
                 cp_async<16>(v0 + at, (const uint8_t*)a.v_cache + off, n);
             }
