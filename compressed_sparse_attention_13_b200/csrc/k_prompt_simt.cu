@@ -108,21 +108,20 @@ __global__ void __launch_bounds__(kThreads * Tile<D>::kGroups, D == 64 ? 2 : 1) 
     float* const sk = sq + kRows * LDK + g * Tile<D>::kGroup;
     float* const sv = sk + kKeys * LDK;
     float* const sp = sv + kKeys * D;
-    __shared__ int s_seq, s_tile;
+    __shared__ SeqTile tile;
     const int tx = tid & 15, ty = tid >> 4, lane = threadIdx.x & 31;
     if (threadIdx.x < 32) {
-        int s, tile;
-        find_tile(a.cu_q, a.n_seq, kRows, int(blockIdx.x / unsigned(a.H)), lane, s, tile);
-        if (lane == 0) { s_seq = s; s_tile = tile; }
+        const SeqTile t = find_tile(a.cu_q, a.cu_k, a.n_seq, kRows, int(blockIdx.x / unsigned(a.H)), lane);
+        if (lane == 0) tile = t;
     }
     __syncthreads();
-    if (s_seq < 0) return;
+    if (tile.s < 0) return;
     const int h = int(blockIdx.x % unsigned(a.H)), hk = h / (a.H / a.HK);
-    const int64_t q0 = a.cu_q[s_seq], k0 = a.cu_k[s_seq];
-    const int full_q = a.cu_q[s_seq + 1] - int(q0), len_k = a.cu_k[s_seq + 1] - int(k0);
+    const int64_t q0 = tile.q0, k0 = tile.k0;
+    const int full_q = tile.len_q, len_k = tile.len_k;
     const int len_q = int(min(int64_t(full_q), a.n_q - q0));
     const int nk = int(max(min(k0 + len_k, a.n_k) - k0, int64_t(0)));
-    const int off = len_k - full_q, tok0 = s_tile * kRows;
+    const int off = len_k - full_q, tok0 = tile.tile * kRows;
     const int tok_last = min(tok0 + kRows, len_q) - 1;
     const int t_first = min(tok0 + off, nk - 1), t_last = min(tok_last + off, nk - 1);
     const int lo_first = a.W > 0 ? max(tok0 + off - a.W + 1, 0) : 0, lo_last = a.W > 0 ? max(tok_last + off - a.W + 1, 0) : 0;

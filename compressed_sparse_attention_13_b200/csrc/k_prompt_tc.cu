@@ -6,7 +6,7 @@
 // A q tile is 128 rows of one key / value head: floor(128 / G) tokens times
 // the G query heads that share the head, so that a K / V tile serves all of
 // them and short sequences fill the rows.  A CTA owns NQ q tiles of
-// consecutive tokens (two for d <= 128, one above) and walks the keys that
+// consecutive tokens (two at d = 128, else one) and walks the keys that
 // any of its rows sees in tiles of 64, with the running maximum and sum of
 // each row in the thread that owns the row; P never leaves the SM.
 //
@@ -63,11 +63,16 @@ constexpr int kMaxGuarded = 9;
 
 template <int D>
 struct Cfg {
-    static constexpr int NQ = D <= 128 ? 2 : 1;      // q tiles of a CTA
+    // q tiles of a CTA, CTAs of an SM: at d = 128 a K / V tile serves two q tiles
+    // (one, and two CTAs an SM: 37% slower on one long prompt); at d = 64 two
+    // CTAs are 3 to 8% faster, one's start and end are covered by the other.
+    static constexpr int NQ = D == 128 ? 2 : 1;
+    static constexpr int kCtas = D == 64 ? 2 : 1;
     static constexpr int BN = 64;                    // keys of a tile
     static constexpr int kSlots = 2;                 // S slots of a q tile
     static constexpr int NS = D <= 128 ? 4 : D == 192 ? 3 : 2;  // stages of the K and of the V ring
     static constexpr int kThreads = NQ * 128 + 128;
+    static constexpr int kTmem = 512 / kCtas;        // columns
     static constexpr int kQBytes = 128 * D * 2;
     static constexpr int kTileBytes = BN * D * 2;
 };
@@ -82,7 +87,8 @@ struct Smem {
     uint64_t g_full[C::NS], v_ok[C::NS];  // guarded tiles: landed, cleared
     uint64_t s_full[2 * C::NQ], p_full[2 * C::NQ], o_done[2 * C::NQ], o_full[C::NQ], guard_done;
     uint32_t tmem_base;
-    int seq, tile, bad;
+    SeqTile tile;
+    int bad;
     uint32_t bad_rows[kMaxGuarded][C::BN / 32];  // guarded tiles' rows with non-finite values
     int guarded_at[kMaxGuarded];                 // the guarded tiles' first keys
 };
@@ -154,7 +160,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }  // namespace
 
 template <int D>
-__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
     prompt_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, const PromptArgs a) {
     using C = Cfg<D>;
@@ -168,10 +174,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_suspended<false>(bar, parity, a.status); };
     auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_suspended<true>(bar, parity, a.status); };
 
-    if (warp == 0) {
-        int s, tile;
-        find_tile(a.cu_q, a.n_seq, NQ * tpt, int(blockIdx.x / unsigned(a.HK)), lane, s, tile);
-        if (lane == 0) { S.seq = s; S.tile = tile; }
+    if (warp == kTma) {
+        const SeqTile t = find_tile(a.cu_q, a.cu_k, a.n_seq, NQ * tpt, int(blockIdx.x / unsigned(a.HK)), lane);
+        if (lane == 0) S.tile = t;
     }
     if (threadIdx.x == 32) {
         for (int i = 0; i < NQ; ++i) { mbar_init(&S.q_full[i], 1); mbar_init(&S.o_full[i], 1); }
@@ -194,30 +199,28 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         prefetch_tmap(&map_k);
         prefetch_tmap(&map_v);
     }
-    if (warp == kMma) { tmem_alloc(&S.tmem_base, 512); tmem_relinquish(); }
+    if (warp == kMma) { tmem_alloc(&S.tmem_base, C::kTmem); tmem_relinquish(); }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // All 512 columns are allocated, so they begin at column 0: a constant, which
+    // Where all 512 columns are allocated they begin at column 0: a constant, which
     // keeps the tensor instructions' addresses out of the registers.
-    constexpr uint32_t tmem = 0;
-    if (S.tmem_base != 0 && threadIdx.x == 0) atomicOr(a.status, CSA_DEV_TIMEOUT);
-    constexpr uint32_t tO = tmem + NQ * 128;  // S slots at tmem + slot * BN, O of q tile i at tO + i * D
+    const uint32_t tmem = C::kTmem == 512 ? 0u : S.tmem_base;
+    const uint32_t tO = tmem + NQ * 128;  // S slots at tmem + slot * BN, O of q tile i at tO + i * D
 
     Work w;
     int n_t[NQ];    // key tiles of each q tile
     int n_max = 0;
-    const int seq = S.seq;
+    const int seq = S.tile.s;
     if (seq >= 0) {
         w.hk = int(blockIdx.x % unsigned(a.HK));
-        w.q0 = a.cu_q[seq];
-        const int len_q = a.cu_q[seq + 1] - int(w.q0);
+        w.q0 = S.tile.q0;
+        const int len_q = S.tile.len_q, len_k = S.tile.len_k;
         w.len_q = int(min(int64_t(len_q), a.n_q - w.q0));
-        w.k0 = a.cu_k[seq];
-        const int len_k = a.cu_k[seq + 1] - int(w.k0);
+        w.k0 = S.tile.k0;
         w.nk = int(max(min(w.k0 + len_k, a.n_k) - w.k0, int64_t(0)));
         w.off = len_k - len_q;
-        w.tok0 = S.tile * NQ * tpt;
+        w.tok0 = S.tile.tile * NQ * tpt;
         w.kb0 = a.W > 0 ? max(w.tok0 + w.off - a.W + 1, 0) : 0;
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
@@ -507,7 +510,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             f = den == 0.f ? 0.f : f / den;
             if (n > 0 && ok) ok = wait_warp(&S.o_full[i], 0) && wait_warp(&S.guard_done, 0);
             tc_fence_after();
-            __nv_bfloat16* out = (__nv_bfloat16*)a.out + ((w.q0 + tok) * a.H + h) * int64_t(D);
+            // The warp's rows go through its part of the q tile, which nothing reads any more (where the tile has no
+            // keys q may still be under way: it is waited for), so that whole rows are written: a row a lane, 16 bytes
+            // an instruction, took 4,000 clocks of a CTA.
+            if (n == 0 && i == 0 && n_max > 0) wait_warp(&S.q_full[0], 0);
+            uint4* const stage = reinterpret_cast<uint4*>(S.q[i] + (warp & 3) * (32 * D * 2));
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
@@ -531,23 +538,30 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                         }
                     }
                 }
-                if (live) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t y[4];
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t y[4];
 #pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            y[g] = bf16x2(__uint_as_float(o[8 * e + 2 * g]) * f, __uint_as_float(o[8 * e + 2 * g + 1]) * f);
-                        *reinterpret_cast<uint4*>(out + 32 * c + 8 * e) = make_uint4(y[0], y[1], y[2], y[3]);
-                    }
+                    for (int g = 0; g < 4; ++g)
+                        y[g] = bf16x2(__uint_as_float(o[8 * e + 2 * g]) * f, __uint_as_float(o[8 * e + 2 * g + 1]) * f);
+                    stage[lane * (D / 8) + ((4 * c + e) ^ (lane & 7))] = make_uint4(y[0], y[1], y[2], y[3]);
                 }
+            }
+            __syncwarp();
+            const int mine = live ? int((w.q0 + tok) * a.H + h) : -1;  // row of the output
+#pragma unroll 4
+            for (int x = lane; x < 32 * (D / 8); x += 32) {
+                const int rr = x / (D / 8), ch = x % (D / 8);
+                const int to = __shfl_sync(0xffffffffu, mine, rr);
+                if (to >= 0)
+                    reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + int64_t(to) * D)[ch] = stage[rr * (D / 8) + (ch ^ (rr & 7))];
             }
         }
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == kMma) tmem_dealloc(tmem, 512);
+    if (warp == kMma) tmem_dealloc(tmem, C::kTmem);
 }
 
 bool prompt_tc_supported(const PromptArgs& a) {
