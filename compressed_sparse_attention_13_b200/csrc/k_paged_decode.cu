@@ -16,7 +16,12 @@
 // The split over the blocks and the copies: paged_split.cuh.  A warp's tile is
 // 16 tokens.  The running maximum of a head is raised only when a tile exceeds
 // it by more than 8 in log2 units (one vote a tile otherwise), sums stay per
-// lane until the unit ends.
+// lane until the unit ends.  P is rounded to the 16-bit type of the MMAs (bf16;
+// f16 for FP8 entries).
+//
+// 32 sequences of up to 11,073 tokens, 32 heads over 8 (682 MB): 115 us, 5.9 TB/s;
+// four of up to 131,072, 64 heads over 8 (1752 MB): 266 us, 6.6 TB/s; 16 of up to
+// 32,768 in FP8, 32 heads over 8 (1006 MB): 180 us, 5.6 TB/s.
 //
 // FP8 entries (E4M3 codes, fp32 scale per 64 channels) are converted to f16
 // exactly, one instruction per pair, and the MMAs run in f16: the query is

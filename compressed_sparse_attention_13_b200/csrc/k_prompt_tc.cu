@@ -33,12 +33,14 @@
 //
 // At d = 128 a pair of q tiles and 64 keys is 1024 clocks of MMA, about 1280 of
 // shared-memory reads for it (q is read again for every 64 keys) and, with 16
-// exponentials a clock, 1024 clocks of those; the softmax takes a quarter of
-// the exponentials by a polynomial on the FMA pipes (exp2_poly; none: 1% more
-// time at 16,384 tokens, half of them: 5% more).  Key tiles of 128 with one S
-// slot cost the same on one long prompt and 11% more on a packed batch of
-// short ones.  16,384 tokens, 32 heads over 8: 2.09 ms, 1.05 PFLOP/s, at the
-// board's power limit (1.57 GHz; 1.84 ms in the first milliseconds).
+// exponentials a clock, 1024 clocks of those; the chain from S over P to the
+// next S makes it about 1700.  What was tried and took longer: a quarter of the
+// exponentials by a polynomial on the FMA pipes (1 to 5% longer but for short
+// prompts, 2% shorter), two threads a row, key tiles of 128 with one S slot (the
+// same on one long prompt, 11% longer on a packed batch of short ones), and a
+// persistent CTA that loads and multiplies the next tile under the end of this
+// one (1% shorter on a packed batch, 5% longer on one prompt).  16,384 tokens,
+// 32 heads over 8: 2.03 ms, 1.08 PFLOP/s, at the board's power limit.
 //
 // Waits are bounded (sm100.cuh).  Compiled as a whole program: setmaxnreg
 // moves registers from the other warps to the softmax.
@@ -131,25 +133,6 @@ struct Work {
     int tok0, hk;
     int kb0;           // first key of the first tile
 };
-
-// 2^y for two y <= 16, on the FMA and integer pipes: y = n + f with n the
-// integer below, 2^f by a cubic through f = 0 and 1 (the smallest largest
-// relative error, 1.0e-4, a twentieth of the rounding of P to bf16), n added to
-// the exponent.  y is raised to -127, where the result is 0; infinities and NaN
-// come out as anything (their rows are set to NaN as a whole).
-__device__ __forceinline__ uint64_t exp2_poly(uint64_t y) {
-    constexpr float kBig = 12582912.f;  // 1.5 * 2^23: its last place is 1
-    constexpr float c1 = 0.69542435f, c2 = 0.22630768f, c3 = 0.07826797f;
-    y = pack2(fmaxf(lo2(y), -127.f), fmaxf(hi2(y), -127.f));
-    uint64_t n, f, p;
-    asm("add.rm.f32x2 %0, %1, %2;" : "=l"(n) : "l"(y), "l"(pack2(kBig, kBig)));
-    f = add2(y, fma2(n, pack2(-1.f, -1.f), pack2(kBig, kBig)));
-    p = fma2(f, pack2(c3, c3), pack2(c2, c2));
-    p = fma2(f, p, pack2(c1, c1));
-    p = fma2(f, p, pack2(1.f, 1.f));
-    return pack2(__uint_as_float(__float_as_uint(lo2(p)) + (__float_as_uint(lo2(n)) << 23)),
-                 __uint_as_float(__float_as_uint(hi2(p)) + (__float_as_uint(hi2(n)) << 23)));
-}
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
@@ -487,9 +470,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const uint64_t y = fma2(pack2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), s2, n2);
-                        const uint64_t z = (e & 3) == 3 ? exp2_poly(y) : pack2(ex2(lo2(y)), ex2(hi2(y)));
+                        const uint64_t z = pack2(ex2(lo2(y)), ex2(hi2(y)));
                         sum[e & 1] = add2(sum[e & 1], z);
-                        p[e] = bf16x2(lo2(z), hi2(z));
+                        p[e] = bf16x2(lo2(z), hi2(z));  // P is rounded to bf16, the type that V takes it in
                     }
                     tmem_st16(tS + 16 * c, p);
                 }

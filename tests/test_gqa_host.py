@@ -138,3 +138,15 @@ def test_a_paged_layer_hands_out_and_takes_back_pages():
     assert lay.lens == [0, 9] and lay.pos.tolist() == [-1, 8] and (lay.table[1] >= 0).sum() == 3
     with pytest.raises(RuntimeError, match="no room"):
         lay.reserve(1, 8)   # the pool has pages left, the table has not
+
+
+def test_the_binding_refuses_tensors_of_different_devices():
+    class On:
+        def __init__(self, i):
+            self.i, self.device = i, f"cuda:{i}"
+
+        def get_device(self):
+            return self.i
+
+    with pytest.raises(ValueError, match="cuda:0, cuda:1"):
+        K._launch("paged_decode_attn", P(), 1, (), None, On(0), None, On(0), On(1))
