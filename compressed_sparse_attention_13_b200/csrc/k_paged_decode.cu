@@ -56,7 +56,7 @@ struct Dec {
     static constexpr int kJoin = kJoinDims + 4;          // padded row of the join buffer
     static constexpr int kRing = kNW * kStages * kTile;
     static constexpr int kSmem = kRing + kNW * 8 * kJoin * 4;
-    static constexpr int kCtas = 2 * (kSmem + 3072) <= 228 * 1024 ? 2 : 1;  // per SM
+    static constexpr int kCtas = 2 * (kSmem + 2048 + kAlignSmem) <= 228 * 1024 ? 2 : 1;  // per SM
     static constexpr int kSlot = kHeads * (D + 2);       // floats of a partial: (m, l) per head, O
 };
 

@@ -36,7 +36,7 @@ struct Dec {
     static constexpr int kRing = kNW * kStages * kTile;
     static constexpr int kJoinDims = D > 64 ? D / 2 : D;
     static constexpr int kSmem = kRing + (NH * D + kNW * NH * kJoinDims + kNW * kTok * NH) * 4;
-    static constexpr int kCtas = 2 * (kSmem + 3072) <= 228 * 1024 ? 2 : 1;  // per SM
+    static constexpr int kCtas = 2 * (kSmem + 2048 + kAlignSmem) <= 228 * 1024 ? 2 : 1;  // per SM
 };
 
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
@@ -297,7 +297,7 @@ size_t paged_decode_simt_workspace(int H, int HK, int D, int64_t batch, int64_t 
 template <int D, int FMT, int NH>
 static cudaError_t launch_nh(const PagedDecodeArgs& a, void* ws, cudaStream_t s) {
     using C = Dec<D, FMT, NH>;
-    static_assert(C::kStages >= 2 && C::kStages <= 8 && C::kStep == kStepSimt && C::kSmem <= 227 * 1024 - 3072, "tile");
+    static_assert(C::kStages >= 2 && C::kStages <= 8 && C::kStep == kStepSimt && C::kSmem <= 227 * 1024 - 2048 - kAlignSmem, "tile");
     const DecodeLayout w = decode_layout(a.H, a.HK, D, a.batch, a.max_pages * a.page_size, a.invariant, NH, C::kStep);
     JoinRec* recs = (JoinRec*)ws;
     float* slots = (float*)((char*)ws + w.rec_bytes);

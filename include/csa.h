@@ -513,6 +513,8 @@ int paged_append(const csa_gqa_params* p, int32_t n_seq, int64_t n_tokens, const
  *   out:       [batch][H][d] in act_fmt
  *   workspace: >= csa_gqa_workspace_size(p, CSA_OP_PAGED_DECODE, batch, batch,
  *              max_pages * page_size)
+ * Limits: max_pages * page_size < 2^31, n_pages * HK * page_size < 2^32 (cache
+ * rows; their bytes may pass 32 bits), batch * H < 2^31.
  * ------------------------------------------------------------------------ */
 int paged_decode_attn(const csa_gqa_params* p, int32_t batch, const void* q, int64_t q_ld,
                       const void* k_cache, const float* k_scales, const void* v_cache,

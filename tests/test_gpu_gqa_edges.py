@@ -239,3 +239,25 @@ def test_attend_reference_of_one_key_is_its_value():
     o, _ = attend(torch.randn(1, 2, 64, dtype=torch.float64), torch.randn(1, 1, 64, dtype=torch.float64), v, 0.1,
                   torch.ones(1, 1, dtype=torch.bool), None, torch.float32, 0.0)
     assert torch.equal(o, v.expand(1, 2, 64))
+
+
+def test_prompts_replayed_from_a_graph_with_other_lengths():
+    """The lengths are read on the device: a captured call serves any batch that fits its buffers."""
+    g = gen(60)
+    p = make(4, 2, 128)
+    n, n_seq = 700, 5
+    q, k, v = (normal(g, n, h, 128, dt=torch.bfloat16).cuda() for h in (4, 2, 2))
+    cu, out = torch.zeros(n_seq + 1, dtype=torch.int32, device="cuda"), torch.zeros_like(q)
+    ws = torch.empty(K.gqa_workspace_size(p, K.OP_PROMPT_ATTN, n_seq, n, 0), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        K.prompt_attn(p, n_seq, q, k, v, cu, cu, None, out, ws)
+    for lens in ([700, 0, 0, 0, 0], [1, 2, 3, 4, 5], [0, 130, 0, 257, 313], [140] * 5):
+        at = torch.tensor([sum(lens[:i]) for i in range(n_seq + 1)], dtype=torch.int32)
+        cu.copy_(at)
+        out.fill_(9)
+        graph.replay()
+        ref, tol = prompt_reference(p, q.cpu(), k.cpu(), v.cpu(), at, at, None, "bf16")
+        m = sum(lens)
+        assert_within(out[:m], ref[:m], tol[:m], str(lens))
+        assert (out[m:] == 9).all()

@@ -150,3 +150,10 @@ def test_the_binding_refuses_tensors_of_different_devices():
 
     with pytest.raises(ValueError, match="cuda:0, cuda:1"):
         K._launch("paged_decode_attn", P(), 1, (), None, On(0), None, On(0), On(1))
+
+
+@pytest.mark.parametrize("kw,want", [(dict(max_pages=1 << 27), -3), (dict(n_pages=1 << 27), -3), (dict(max_pages=(1 << 27) - 1, wb=0), -4),
+                                     (dict(n_pages=(1 << 27) - 1, wb=0), -4)])
+def test_decode_counts_rows_in_32_bits(kw, want):
+    """Pages of 16 tokens and two key heads: 2^27 of them are one too many, either way."""
+    assert decode(P(), **kw) == want
