@@ -363,79 +363,109 @@ def _dense(t, shape, dtype, name):
     return _p(t)
 
 
-def _caches(p, k_cache, v_cache, block_table, n_seq):
-    n_pages, hk, page, d = k_cache.data.shape[0], p.n_kv_heads, p.page_size, p.head_dim
-    fmt = p.cache_fmt
-    dtype = _dtype(fmt if fmt in (F32, BF16) else FP8_S64)
+def _check(dev, *specs):
+    """Pointers of dense tensors of one device, each given as (tensor or None, shape, type, name)."""
     ptrs = []
-    for st, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if st.fmt != fmt:
-            raise ValueError(f"{name} is stored in format {st.fmt}, the parameters name {fmt}")
-        ptrs.append(_dense(st.data, (n_pages, hk, page, d), dtype, name))
-        ptrs.append(_dense(st.scales, (n_pages, hk, page, d // 64), _dtype(F32), name + " scales")
-                    if fmt == FP8_S64 else None)
+    for spec in specs:
+        t = spec[0]
+        if t is None:
+            ptrs.append(None)
+        elif t.shape == spec[1] and t.dtype is spec[2] and t.get_device() == dev and t.is_contiguous():
+            ptrs.append(t.data_ptr())
+        else:
+            _dense(*spec)
+            raise ValueError(f"tensors on different devices: {spec[3]} on {t.device}, another on cuda:{dev}")
+    return ptrs
+
+
+def _cache_specs(p, hk, d, k_cache, v_cache, block_table, n_seq):
+    """What _check is to see of a paged cache, in the calls' order, without the counts."""
+    fmt = p.cache_fmt
+    if k_cache.fmt != fmt or v_cache.fmt != fmt:
+        raise ValueError(f"the caches are stored in formats {k_cache.fmt}, {v_cache.fmt}, the parameters name {fmt}")
     if block_table.dim() != 2 or block_table.shape[0] != n_seq:
         raise ValueError(f"block_table must be [{n_seq}][max_pages], got {list(block_table.shape)}")
-    max_pages = block_table.shape[1]
-    table = _dense(block_table, (n_seq, max_pages), _dtype("i32"), "block_table")
-    return (*ptrs, n_pages, table, max_pages)
+    n_pages, page = k_cache.data.shape[0], p.page_size
+    rows, dtype = (n_pages, hk, page, d), _dtype(fmt if fmt in (F32, BF16) else FP8_S64)
+    ks = vs = scales = None
+    if fmt == FP8_S64:
+        ks, vs, scales = k_cache.scales, v_cache.scales, (n_pages, hk, page, d // 64)
+        if ks is None or vs is None:
+            raise ValueError("an FP8 cache needs its scales")
+    f32, max_pages = _dtype(F32), block_table.shape[1]
+    return ((k_cache.data, rows, dtype, "k_cache"), (ks, scales, f32, "k_cache scales"), (v_cache.data, rows, dtype, "v_cache"),
+            (vs, scales, f32, "v_cache scales"), (block_table, (n_seq, max_pages), _dtype("i32"), "block_table"), n_pages,
+            max_pages)
 
 
-def _launch(fn, p, n, args, stream, t, *others):
-    """Call an entry point with the device of `t` current (launches and the default stream go by
-    the current device); tensors of another device are refused."""
+def _launch(fn, p, n, args, stream, dev):
+    """Call an entry point with the tensors' device current (launches and the default stream go by
+    the current device)."""
     import torch
-    dev = t.get_device()
-    for o in others:
-        if o is not None and o.get_device() != dev:
-            raise ValueError(f"tensors on different devices: {t.device}, {o.device}")
     call = getattr(_lib or lib(), fn)
     if dev == torch.cuda.current_device():
         s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
-        _ok(fn, call(C.byref(p), n, *args, s))
+        st = call(C.byref(p), n, *args, s)
     else:
         with torch.cuda.device(dev):
-            _ok(fn, call(C.byref(p), n, *args, _s(stream)))
+            st = call(C.byref(p), n, *args, _s(stream))
+    if st:
+        raise CsaError(fn, st)
 
 
 def paged_append(p: GqaParams, n_seq: int, n_tokens: int, cu_q, pos0, q, k, v, inv_freq, q_out, k_out,
                  k_cache: Stored, v_cache: Stored, block_table, stream=None):
     """q [n_tokens][H][d] (or None), k, v [n_tokens][HK][d]; cu_q int32 [n_seq + 1] or None
     (one token per sequence); pos0 int64 [n_seq]; inv_freq float64 [rot_dim / 2] or None."""
-    H, HK, d, act = p.n_heads, p.n_kv_heads, p.head_dim, _act_dtype(p)
-    qp, ql = _rows_of(q, n_tokens, H, p, "q") if q is not None else (None, 0)
+    H, HK, d, act, rot = p.n_heads, p.n_kv_heads, p.head_dim, _act_dtype(p), p.rot_dim
     kp, kl = _rows_of(k, n_tokens, HK, p, "k")
     vp, vl = _rows_of(v, n_tokens, HK, p, "v")
-    rot = p.rot_dim
-    args = (n_tokens, _dense(cu_q, (n_seq + 1,), _dtype("i32"), "cu_q"), _dense(pos0, (n_seq,), _dtype("i64"), "pos0"),
-            qp, ql, kp, kl, vp, vl, _dense(inv_freq, (rot // 2,), _dtype("f64"), "inv_freq") if rot > 0 else None,
-            _dense(q_out, (n_tokens, H, d), act, "q_out"), _dense(k_out, (n_tokens, HK, d), act, "k_out"),
-            *_caches(p, k_cache, v_cache, block_table, n_seq))
-    _launch("paged_append", p, n_seq, args, stream, k, q, v, cu_q, pos0, inv_freq, q_out, k_out, k_cache.data,
-            k_cache.scales, v_cache.data, v_cache.scales, block_table)
+    qp, ql = _rows_of(q, n_tokens, H, p, "q") if q is not None else (None, 0)
+    dev = k.get_device()
+    if v.get_device() != dev or (q is not None and q.get_device() != dev):
+        raise ValueError("tensors on different devices: q, k, v")
+    kc, ks, vc, vs, table, n_pages, max_pages = _cache_specs(p, HK, d, k_cache, v_cache, block_table, n_seq)
+    cu, pos, f, qo, ko, kc, ks, vc, vs, table = _check(
+        dev, (cu_q, (n_seq + 1,), _dtype("i32"), "cu_q"), (pos0, (n_seq,), _dtype("i64"), "pos0"),
+        (inv_freq if rot > 0 else None, (rot // 2,), _dtype("f64"), "inv_freq"), (q_out, (n_tokens, H, d), act, "q_out"),
+        (k_out, (n_tokens, HK, d), act, "k_out"), kc, ks, vc, vs, table)
+    _launch("paged_append", p, n_seq, (n_tokens, cu, pos, qp, ql, kp, kl, vp, vl, f, qo, ko, kc, ks, vc, vs, n_pages, table,
+                                       max_pages), stream, dev)
 
 
 def paged_decode_attn(p: GqaParams, batch: int, q, k_cache: Stored, v_cache: Stored, block_table, q_pos, sinks,
                       out, workspace, stream=None):
     """q, out [batch][H][d]; q_pos int64 [batch]; sinks float32 [H] or None."""
-    qp, ql = _rows_of(q, batch, p.n_heads, p, "q")
-    wp, wb = _ws(workspace)
-    args = (qp, ql, *_caches(p, k_cache, v_cache, block_table, batch), _dense(q_pos, (batch,), _dtype("i64"), "q_pos"),
-            _dense(sinks, (p.n_heads,), _dtype(F32), "sinks"),
-            _dense(out, (batch, p.n_heads, p.head_dim), _act_dtype(p), "out"), wp, wb)
-    _launch("paged_decode_attn", p, batch, args, stream, q, k_cache.data, k_cache.scales, v_cache.data, v_cache.scales,
-            block_table, q_pos, sinks, out, workspace)
+    H, HK, d = p.n_heads, p.n_kv_heads, p.head_dim
+    qp, ql = _rows_of(q, batch, H, p, "q")
+    dev = q.get_device()
+    kc, ks, vc, vs, table, n_pages, max_pages = _cache_specs(p, HK, d, k_cache, v_cache, block_table, batch)
+    kc, ks, vc, vs, table, pos, snk, o, w = _check(
+        dev, kc, ks, vc, vs, table, (q_pos, (batch,), _dtype("i64"), "q_pos"), (sinks, (H,), _dtype(F32), "sinks"),
+        (out, (batch, H, d), q.dtype, "out"), _ws_spec(workspace))
+    _launch("paged_decode_attn", p, batch, (qp, ql, kc, ks, vc, vs, n_pages, table, max_pages, pos, snk, o, w,
+                                            _ws_bytes(workspace)), stream, dev)
+
+
+def _ws_spec(ws):
+    return (None,) if ws is None else (ws, ws.shape, ws.dtype, "workspace")
+
+
+def _ws_bytes(ws):
+    return 0 if ws is None else ws.nbytes
 
 
 def prompt_attn(p: GqaParams, n_seq: int, q, k, v, cu_q, cu_k, sinks, out, workspace, stream=None):
     """q, out [n_q][H][d], k, v [n_k][HK][d]; cu_q, cu_k int32 [n_seq + 1]; sinks float32 [H]
     or None."""
-    n_q, n_k = q.shape[0], k.shape[0]
-    qp, ql = _rows_of(q, n_q, p.n_heads, p, "q")
-    kp, kl = _rows_of(k, n_k, p.n_kv_heads, p, "k")
-    vp, vl = _rows_of(v, n_k, p.n_kv_heads, p, "v")
-    wp, wb = _ws(workspace)
-    args = (qp, ql, n_q, kp, kl, vp, vl, n_k, _dense(cu_q, (n_seq + 1,), _dtype("i32"), "cu_q"),
-            _dense(cu_k, (n_seq + 1,), _dtype("i32"), "cu_k"), _dense(sinks, (p.n_heads,), _dtype(F32), "sinks"),
-            _dense(out, (n_q, p.n_heads, p.head_dim), _act_dtype(p), "out"), wp, wb)
-    _launch("prompt_attn", p, n_seq, args, stream, q, k, v, cu_q, cu_k, sinks, out, workspace)
+    n_q, n_k, H, HK, i32 = q.shape[0], k.shape[0], p.n_heads, p.n_kv_heads, _dtype("i32")
+    qp, ql = _rows_of(q, n_q, H, p, "q")
+    kp, kl = _rows_of(k, n_k, HK, p, "k")
+    vp, vl = _rows_of(v, n_k, HK, p, "v")
+    dev = q.get_device()
+    if k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("tensors on different devices: q, k, v")
+    cq, ck, snk, o, w = _check(dev, (cu_q, (n_seq + 1,), i32, "cu_q"), (cu_k, (n_seq + 1,), i32, "cu_k"),
+                               (sinks, (H,), _dtype(F32), "sinks"), (out, (n_q, H, p.head_dim), q.dtype, "out"),
+                               _ws_spec(workspace))
+    _launch("prompt_attn", p, n_seq, (qp, ql, n_q, kp, kl, vp, vl, n_k, cq, ck, snk, o, w, _ws_bytes(workspace)), stream, dev)

@@ -534,6 +534,11 @@ bool paged_decode_tc_supported(int act, int cache) {
     return act == CSA_BF16 && (cache == CSA_BF16 || cache == CSA_FP8_S64);
 }
 
+bool one_piece(const PagedDecodeArgs& a) {
+    const int64_t most = a.max_pages * a.page_size;
+    return (a.W > 0 ? std::min<int64_t>(a.W, most) : most) <= 256;
+}
+
 void set_page_division(PagedDecodeArgs* a) {
     int s = 0;
     while ((int64_t(1) << s) < a->page_size) ++s;
@@ -570,12 +575,14 @@ size_t paged_decode_workspace(int H, int HK, int D, int64_t batch, int64_t n_ctx
 }
 
 template <int D, bool FP8, int NT>
-static cudaError_t launch_decode(const PagedDecodeArgs& a, void* ws, cudaStream_t s) {
+static cudaError_t launch_decode(PagedDecodeArgs a, void* ws, cudaStream_t s) {
     using C = Dec<D, FP8, NT>;
     static_assert(C::kStages >= 2 && C::kStages <= 8, "stages");
     static_assert(C::kStep == kStepTc, "steps");
     const DecodeLayout w = decode_layout(a.H, a.HK, D, a.batch, a.max_pages * a.page_size, a.invariant, C::kHeads, C::kStep);
-    JoinRec* recs = (JoinRec*)ws;
+    const bool single = one_piece(a);
+    if (single) a.invariant = 1;
+    JoinRec* recs = single ? nullptr : (JoinRec*)ws;
     float* slots = (float*)((char*)ws + w.rec_bytes);
     const int hb = int(w.units / a.HK);
     cudaError_t e = ensure_smem(paged_decode_kernel<D, FP8, NT>, C::kSmem + kAlignSmem);
@@ -583,6 +590,7 @@ static cudaError_t launch_decode(const PagedDecodeArgs& a, void* ws, cudaStream_
     paged_decode_kernel<D, FP8, NT><<<C::kCtas * kNumSMs, 32 * kNW, C::kSmem + kAlignSmem, s>>>(a, int(w.units), hb, recs, slots);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    if (single) return cudaSuccess;
     return launch_paged_join(a, a.invariant ? w.recs : C::kCtas * kNumSMs, hb, C::kHeads, recs, slots, s);
 }
 

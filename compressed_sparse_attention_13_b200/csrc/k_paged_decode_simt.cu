@@ -295,11 +295,13 @@ size_t paged_decode_simt_workspace(int H, int HK, int D, int64_t batch, int64_t 
 }
 
 template <int D, int FMT, int NH>
-static cudaError_t launch_nh(const PagedDecodeArgs& a, void* ws, cudaStream_t s) {
+static cudaError_t launch_nh(PagedDecodeArgs a, void* ws, cudaStream_t s) {
     using C = Dec<D, FMT, NH>;
     static_assert(C::kStages >= 2 && C::kStages <= 8 && C::kStep == kStepSimt && C::kSmem <= 227 * 1024 - 2048 - kAlignSmem, "tile");
     const DecodeLayout w = decode_layout(a.H, a.HK, D, a.batch, a.max_pages * a.page_size, a.invariant, NH, C::kStep);
-    JoinRec* recs = (JoinRec*)ws;
+    const bool single = one_piece(a);
+    if (single) a.invariant = 1;
+    JoinRec* recs = single ? nullptr : (JoinRec*)ws;
     float* slots = (float*)((char*)ws + w.rec_bytes);
     const int hb = int(w.units / a.HK);
     cudaError_t e = ensure_smem(paged_decode_simt_kernel<D, FMT, NH>, C::kSmem + kAlignSmem);
@@ -307,6 +309,7 @@ static cudaError_t launch_nh(const PagedDecodeArgs& a, void* ws, cudaStream_t s)
     paged_decode_simt_kernel<D, FMT, NH><<<C::kCtas * kNumSMs, 32 * kNW, C::kSmem + kAlignSmem, s>>>(a, int(w.units), hb, recs, slots);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    if (single) return cudaSuccess;
     return launch_paged_join(a, a.invariant ? w.recs : C::kCtas * kNumSMs, hb, NH, recs, slots, s);
 }
 

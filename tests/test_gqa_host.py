@@ -142,14 +142,26 @@ def test_a_paged_layer_hands_out_and_takes_back_pages():
 
 def test_the_binding_refuses_tensors_of_different_devices():
     class On:
+        is_cuda, shape, dtype = True, (2,), torch.int32
+
         def __init__(self, i):
             self.i, self.device = i, f"cuda:{i}"
 
         def get_device(self):
             return self.i
 
-    with pytest.raises(ValueError, match="cuda:0, cuda:1"):
-        K._launch("paged_decode_attn", P(), 1, (), None, On(0), None, On(0), On(1))
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return 16 * self.i
+
+    spec = ((2,), torch.int32, "cu_q")
+    assert K._check(1, (On(1), *spec), (None, *spec), (On(1), *spec)) == [16, None, 16]
+    with pytest.raises(ValueError, match="different devices: cu_q on cuda:0, another on cuda:1"):
+        K._check(1, (On(1), *spec), (On(0), *spec))
+    with pytest.raises(ValueError, match="int64"):
+        K._check(1, (On(1), (2,), torch.int64, "cu_q"))
 
 
 @pytest.mark.parametrize("kw,want", [(dict(max_pages=1 << 27), -3), (dict(n_pages=1 << 27), -3), (dict(max_pages=(1 << 27) - 1, wb=0), -4),
