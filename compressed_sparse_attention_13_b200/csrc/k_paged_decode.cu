@@ -409,6 +409,14 @@ __global__ void __launch_bounds__(32 * kNW, Dec<D, FP8, NT>::kCtas)
                 for (int z = 4; z < 32; z <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], z);
                 if (g == 0) jml[warp][8 * nt + 2 * c4 + i] = make_float2(m[nt][i], l[nt][i]);
             }
+        if constexpr (FP8) {  // from here on what O is multiplied by (2^-100 .. 2^100); a division an element took 5 us a unit
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int gr = 0; gr < C::kGroups; ++gr)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) f[nt][gr][i] = __frcp_rn(f[nt][gr][i]);
+        }
         const bool whole = b == 0 && e == cur.v.steps;
         const int64_t slot = part_slot(a, plan, cur, units, weight<C::kStep>(a, cur.v), b == 0, whole, recs);
 #pragma unroll
@@ -421,7 +429,7 @@ __global__ void __launch_bounds__(32 * kNW, Dec<D, FP8, NT>::kCtas)
                     const int k = k0 + kk;
                     const int dim = 16 * kk + (FP8 ? 2 * g + (i >> 1) : g + 8 * (i >> 1));
                     float x = o[nt][k][i];
-                    if constexpr (FP8) x = x == 0.f ? 0.f : x / f[nt][k / 4][i & 1];
+                    if constexpr (FP8) x *= f[nt][k / 4][i & 1];
                     jo[(warp * 8 + 2 * c4 + (i & 1)) * C::kJoin + dim] = x;
                 }
             __syncthreads();
