@@ -138,6 +138,10 @@ __global__ void __launch_bounds__(32 * kNW, Dec<D, FP8, NT>::kCtas)
     while (cur.x < cur.x1) {
         int b, e, dx;
         piece_of<C::kStep>(a, cur, b, e, dx);
+        if (b >= e) {
+            advance<C::kStep>(a, units, cur, dx);
+            continue;
+        }
         if (threadIdx.x == 0 && a.q_pos[cur.s] >= a.max_pages * a.page_size) flag_status(CSA_DEV_BAD_INDEX);
         const int hk = cur.u / hb, head0 = (cur.u % hb) * C::kHeads;  // within the group of G
         const int n_heads = min(C::kHeads, G - head0);

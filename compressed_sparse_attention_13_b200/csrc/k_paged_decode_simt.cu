@@ -122,6 +122,10 @@ __global__ void __launch_bounds__(32 * kNW, Dec<D, FMT, NH>::kCtas)
     while (cur.x < cur.x1) {
         int b, e, dx;
         piece_of<C::kStep>(a, cur, b, e, dx);
+        if (b >= e) {
+            advance<C::kStep>(a, units, cur, dx);
+            continue;
+        }
         if (threadIdx.x == 0 && a.q_pos[cur.s] >= a.max_pages * a.page_size) flag_status(CSA_DEV_BAD_INDEX);
         const int hk = cur.u / hb, head0 = (cur.u % hb) * NH;  // within the group of G
         const int n_heads = min(NH, G - head0);

@@ -4,8 +4,8 @@
 // tensor cores, k_paged_decode_simt.cu on the CUDA cores).
 //
 // Work is dealt in steps of STEP visible tokens of one unit (sequence, head
-// group): the steps of all units are laid end to end and cut into equal
-// ranges, one per block (persistent, a multiple of the SMs), so ragged batches
+// group): the steps of all units, and kUnitCost more for each, are laid end to
+// end and cut into equal ranges, one per block (persistent, a multiple of the SMs), so ragged batches
 // stay balanced whatever their lengths, which only the device knows.  A unit
 // that lies in one block's range is written at once; the parts of others go to
 // the workspace as (m, l, O) and a small kernel joins them in order.  In batch
@@ -22,6 +22,11 @@ namespace csa {
 
 constexpr int kNW = 4;                 // warps of a block
 constexpr int kMinSteps = 2;           // a block's share is not cut finer than this
+// What a unit costs beside its steps, in steps: its query, its join, its output.
+// 12 / 39 / 30 sequences, most of them short, bf16 at d = 128 / 256 / 64 (us):
+//   cost 0: 30 / 43 / 58,  2: 18 / 26 / 28,  3: 17 / 27 / 25,  6: 17 / 32 / 23
+// (one long row of 32 heads over 8, 1,001 tokens: 10.9 / 11.5 / 11.3 / 11.3).
+constexpr int kUnitCost = 3;
 constexpr uint32_t kNoRow = 0xFFFFFFFFu;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -106,7 +111,7 @@ struct Plan {
 
 template <int STEP>
 __device__ __forceinline__ int weight(const PagedDecodeArgs& a, const Span& v) {
-    if (!a.invariant) return v.steps;
+    if (!a.invariant) return v.steps + kUnitCost;
     const int p = piece_steps<STEP>(v.steps);
     return (v.steps + p - 1) / p;
 }
@@ -173,9 +178,10 @@ __device__ __forceinline__ void piece_of(const PagedDecodeArgs& a, const Cursor&
         e = min(b + p, q.v.steps);
         dx = 1;
     } else {
-        b = q.at;
-        e = int(min(int64_t(q.v.steps), q.at + (q.x1 - q.x)));
-        dx = e - b;
+        // (positions from steps on are the unit's cost: nothing to do, b = e)
+        dx = int(min(int64_t(q.v.steps + kUnitCost - q.at), q.x1 - q.x));
+        b = min(q.at, q.v.steps);
+        e = min(q.at + dx, q.v.steps);
     }
 }
 template <int STEP>
@@ -213,7 +219,14 @@ struct Copier {
                                       uint32_t* vmask_)
         : a(a_), units(units_), hb(hb_), pre(c), ring(ring_), vmask(vmask_) {
         piece_of<C::kStep>(a, pre, pb, pe, pdx);
+        skip_empty();
         lookup();
+    }
+    __device__ __forceinline__ void skip_empty() {
+        while (pb >= pe && pre.x < pre.x1) {
+            advance<C::kStep>(a, units, pre, pdx);
+            if (pre.x < pre.x1) piece_of<C::kStep>(a, pre, pb, pe, pdx);
+        }
     }
     __device__ __forceinline__ void lookup() {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -281,10 +294,8 @@ struct Copier {
                     }
                 }
             }
-            if (++pb >= pe) {
-                advance<C::kStep>(a, units, pre, pdx);
-                if (pre.x < pre.x1) piece_of<C::kStep>(a, pre, pb, pe, pdx);
-            }
+            ++pb;
+            skip_empty();
             lookup();
         }
         cp_commit();
