@@ -19,9 +19,9 @@
 // lane until the unit ends.  P is rounded to the 16-bit type of the MMAs (bf16;
 // f16 for FP8 entries).
 //
-// 32 sequences of up to 11,073 tokens, 32 heads over 8 (682 MB): 115 us, 5.9 TB/s;
-// four of up to 131,072, 64 heads over 8 (1752 MB): 266 us, 6.6 TB/s; 16 of up to
-// 32,768 in FP8, 32 heads over 8 (1006 MB): 180 us, 5.6 TB/s.
+// 32 sequences of up to 11,073 tokens, 32 heads over 8 (682 MB): 110 us, 6.2 TB/s;
+// four of up to 131,072, 64 heads over 8 (1752 MB): 267 us, 6.6 TB/s; 16 of up to
+// 32,768 in FP8, 32 heads over 8 (1006 MB): 181 us, 5.6 TB/s.
 //
 // FP8 entries (E4M3 codes, fp32 scale per 64 channels) are converted to f16
 // exactly, one instruction per pair, and the MMAs run in f16: the query is

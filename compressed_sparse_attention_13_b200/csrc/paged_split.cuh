@@ -5,12 +5,12 @@
 //
 // Work is dealt in steps of STEP visible tokens of one unit (sequence, head
 // group): the steps of all units, and kUnitCost more for each, are laid end to
-// end and cut into equal ranges, one per block (persistent, a multiple of the SMs), so ragged batches
-// stay balanced whatever their lengths, which only the device knows.  A unit
-// that lies in one block's range is written at once; the parts of others go to
-// the workspace as (m, l, O) and a small kernel joins them in order.  In batch
-// invariant mode a unit is cut at multiples of its own piece length instead
-// and the blocks take whole pieces.
+// end and cut into equal ranges, one per block (persistent, a multiple of the
+// SMs), so ragged batches stay balanced whatever their lengths, which only the
+// device knows.  A unit that lies in one block's range is written at once; the
+// parts of others go to the workspace as (m, l, O) and a small kernel joins
+// them in order.  In batch invariant mode a unit is cut at multiples of its own
+// piece length instead and the blocks take whole pieces.
 //
 // In a block each of the four warps takes every fourth tile with its own ring
 // of cp.async stages (no block barrier in the loop); the ring runs on across
