@@ -21,7 +21,7 @@
 //
 // 32 sequences of up to 11,073 tokens, 32 heads over 8 (682 MB): 110 us, 6.2 TB/s;
 // four of up to 131,072, 64 heads over 8 (1752 MB): 267 us, 6.6 TB/s; 16 of up to
-// 32,768 in FP8, 32 heads over 8 (1006 MB): 181 us, 5.6 TB/s.
+// 32,768 in FP8, 32 heads over 8 (1006 MB): 163 us, 6.2 TB/s.
 //
 // FP8 entries (E4M3 codes, fp32 scale per 64 channels) are converted to f16
 // exactly, one instruction per pair, and the MMAs run in f16: the query is
@@ -48,15 +48,20 @@ struct Dec {
     static constexpr int kGroups = D / 64;
     static constexpr int kScaleBytes = FP8 ? kTok * kGroups * 4 : 0;
     static constexpr int kTile = 2 * (kTok * kRow + kScaleBytes);  // K and V of 16 tokens
-    // Stages: about 100 KB a CTA, so that two fit an SM; one CTA of up to 192 KB for the wide heads
-    static constexpr int kBudget = (D <= 128 ? 96 : 192) * 1024;
+    // CTAs an SM, and stages of what shared memory is left for them: as many as the registers allow where the
+    // warps' instructions bound the kernel (FP8; short rows), else two, one where only that leaves two stages.
+    // 16 sequences of up to 32,768 tokens in FP8: d = 64, 138 us with two and 114 with three, d = 128, 178 and
+    // 162 (G = 16: 236 and 252), d = 192, 352 with one and 245 with two, d = 256, 398 and 309; 32 sequences of
+    // up to 11,073 in bf16: d = 64, 67 with two and 63 with three, d = 192, 172 with one and 160 with two.
+    static constexpr int kCtas = D == 256 && !FP8 ? 1 : D <= 128 && (FP8 || D == 64) && NT == 1 ? 3 : 2;
+    static constexpr int kBudget = (kCtas == 3 ? 60 : kCtas == 1 ? 192 : D == 256 ? 90 : 96) * 1024;
     static constexpr int kStages = kBudget / (kNW * kTile) > 8 ? 8 : kBudget / (kNW * kTile);
     static constexpr int kHeads = 8 * NT;
     static constexpr int kJoinDims = D > 64 ? D / 2 : D; // the warps' results are joined in halves of the dims
     static constexpr int kJoin = kJoinDims + 4;          // padded row of the join buffer
     static constexpr int kRing = kNW * kStages * kTile;
     static constexpr int kSmem = kRing + kNW * 8 * kJoin * 4;
-    static constexpr int kCtas = 2 * (kSmem + 2048 + kAlignSmem) <= 228 * 1024 ? 2 : 1;  // per SM
+    static_assert(kCtas * (kSmem + 2048 + kAlignSmem) <= 228 * 1024, "shared memory");
     static constexpr int kSlot = kHeads * (D + 2);       // floats of a partial: (m, l) per head, O
 };
 
@@ -474,7 +479,7 @@ __global__ void __launch_bounds__(32 * kNW, Dec<D, FP8, NT>::kCtas)
 // block joins a quarter of a unit's heads * D outputs: its warps first turn the
 // parts' maxima and sums into weights (a warp per head), then its threads take
 // four dims each and the parts in groups, added in the groups' order.
-constexpr int kJoinThreads = 256, kJoinParts = 2 * kNumSMs;
+constexpr int kJoinThreads = 256, kJoinParts = kMaxCtas * kNumSMs;
 
 __global__ void __launch_bounds__(kJoinThreads)
     paged_decode_join_kernel(const PagedDecodeArgs a, int hb, int heads, const JoinRec* recs, const float* slots) {
@@ -566,7 +571,7 @@ DecodeLayout decode_layout(int H, int HK, int D, int64_t batch, int64_t n_ctx, b
         w.recs = batch * w.units;
         w.slots = batch * w.units * std::min<int64_t>(64, ceil_div(steps, 512 / step) + 1);
     } else {
-        w.recs = 2 * kNumSMs;
+        w.recs = kMaxCtas * kNumSMs;
         w.slots = 2 * w.recs;
     }
     w.rec_bytes = (size_t(w.recs) * sizeof(JoinRec) + 255) & ~size_t(255);

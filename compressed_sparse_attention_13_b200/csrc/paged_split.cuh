@@ -21,6 +21,7 @@
 namespace csa {
 
 constexpr int kNW = 4;                 // warps of a block
+constexpr int kMaxCtas = 3;            // blocks an SM, at most
 constexpr int kMinSteps = 2;           // a block's share is not cut finer than this
 // What a unit costs beside its steps, in steps: its query, its join, its output.
 // 12 / 39 / 30 sequences, most of them short, bf16 at d = 128 / 256 / 64 (us):
