@@ -5,6 +5,11 @@
 
 namespace csa {
 
+// First key that a query at key position t sees with a window of W keys (0: no
+// window).  t may be negative (fewer keys than queries) and W anything up to
+// INT32_MAX, so that t - W + 1 is formed only where it is not below 1.
+__host__ __device__ __forceinline__ int first_seen(int t, int W) { return W > 0 && t >= W ? t - W + 1 : 0; }
+
 // A tile of a packed batch and its sequence: packed rows q0 .. q0 + len_q - 1,
 // keys k0 .. k0 + len_k - 1.
 struct SeqTile {

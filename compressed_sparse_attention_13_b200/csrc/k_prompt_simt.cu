@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreads * Tile<D>::kGroups, D == 64 ? 2 : 1) 
     const int off = len_k - full_q, tok0 = tile.tile * kRows;
     const int tok_last = min(tok0 + kRows, len_q) - 1;
     const int t_first = min(tok0 + off, nk - 1), t_last = min(tok_last + off, nk - 1);
-    const int lo_first = a.W > 0 ? max(tok0 + off - a.W + 1, 0) : 0, lo_last = a.W > 0 ? max(tok_last + off - a.W + 1, 0) : 0;
+    const int lo_first = first_seen(tok0 + off, a.W), lo_last = first_seen(tok_last + off, a.W);
     const float sl2 = a.scale * kLog2e;
     uint64_t o[4][E][2];
     float m[4], l[4];
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads * Tile<D>::kGroups, D == 64 ? 2 : 1) 
         if (cut) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int at = tok0 + 4 * ty + i + off, t = min(at, nk - 1), lo = a.W > 0 ? at - a.W + 1 : 0;
+                const int at = tok0 + 4 * ty + i + off, t = min(at, nk - 1), lo = first_seen(at, a.W);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int key = kb + tx + 16 * j;

@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
         w.nk = int(max(min(w.k0 + len_k, a.n_k) - w.k0, int64_t(0)));
         w.off = len_k - len_q;
         w.tok0 = S.tile.tile * NQ * tpt;
-        w.kb0 = a.W > 0 ? max(w.tok0 + w.off - a.W + 1, 0) : 0;
+        w.kb0 = first_seen(w.tok0 + w.off, a.W);
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
             const int first = w.tok0 + i * tpt, last = min(first + tpt, w.len_q) - 1;
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
         }
         // a tile is guarded if some row of the CTA does not see all of it
         const int t_first = min(w.tok0 + w.off, w.nk - 1), tok_last = min(w.tok0 + NQ * tpt, w.len_q) - 1;
-        const int lo_last = a.W > 0 ? max(tok_last + w.off - a.W + 1, 0) : 0;
+        const int lo_last = first_seen(tok_last + w.off, a.W);
         auto guarded = [&](int j) {
             const int kb = w.kb0 + j * BN;
             return kb + BN - 1 > t_first || kb < lo_last;
@@ -414,10 +414,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
             const int tok = w.tok0 + i * tpt + r / G, h = w.hk * G + r % G;
             const bool live = r < G * tpt && tok < w.len_q;
             const int t = live ? min(tok + w.off, w.nk - 1) : -1;       // last key that the row sees
-            const int lo = a.W > 0 ? max(tok + w.off - a.W + 1, 0) : 0;  // first
+            const int lo = first_seen(tok + w.off, a.W);  // first
             const int t_min = min(w.tok0 + i * tpt + w.off, w.nk - 1);    // of the tile's first token
             const int tl = min(w.tok0 + (i + 1) * tpt, w.len_q) - 1;
-            const int lo_max = a.W > 0 ? max(tl + w.off - a.W + 1, 0) : 0;
+            const int lo_max = first_seen(tl + w.off, a.W);
             const float sl2 = a.scale * kLog2e;
             const uint64_t s2 = pack2(sl2, sl2);
             float m = -INFINITY, l = 0.f;
