@@ -76,15 +76,20 @@ struct Span {
     int n, steps;
 };
 
+// Of a token at t (any 64-bit value: t + 1 and t - W + 1 are formed where they
+// cannot overflow) with places for `cap` tokens.
+template <int STEP>
+__host__ __device__ __forceinline__ Span span_at(int64_t t, int W, int64_t cap) {
+    Span v;
+    v.lo = W > 0 && t >= W ? t - W + 1 : 0;
+    const int64_t hi = t < cap ? t + 1 : cap;
+    v.n = hi > v.lo ? int(hi - v.lo) : 0;
+    v.steps = v.n > 0 ? (v.n - 1) / STEP + 1 : 1;
+    return v;
+}
 template <int STEP>
 __device__ __forceinline__ Span span_of(const PagedDecodeArgs& a, int64_t s) {
-    const int64_t t = a.q_pos[s], cap = a.max_pages * a.page_size;
-    Span v;
-    v.lo = a.W > 0 ? max(t - a.W + 1, int64_t(0)) : 0;
-    const int64_t hi = min(t + 1, cap);
-    v.n = int(max(hi - v.lo, int64_t(0)));
-    v.steps = max((v.n + STEP - 1) / STEP, 1);
-    return v;
+    return span_at<STEP>(a.q_pos[s], a.W, a.max_pages * a.page_size);
 }
 
 // Batch invariant mode: steps of a piece, from the row's own length (at least

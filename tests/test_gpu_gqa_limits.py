@@ -3,10 +3,41 @@ import pytest
 import torch
 
 import compressed_sparse_attention_13_b200 as K
-from gqa_reference import assert_within
-from test_gpu_gqa import clean, gen, make, normal, prompt_data, prompt_reference, run_prompt
+from gqa_reference import assert_within, attend, paged_rows
+from test_gpu_gqa import DT, clean, fill_cache, gen, make, normal, prompt_data, prompt_reference, run_prompt, table_of
 
 pytestmark = pytest.mark.gpu
+
+
+def attend_paged(q, k, v, v_scales, scale, sinks, act, cache):
+    """One query [1][H][d] over the rows k, v [n][HK][d] (float64; v_scales [n][HK][d/64] of FP8 rows): (out, tol).
+
+    P is rounded to 16 bits before the product with v by the kernel for bf16 queries: to bf16 (half a step is 2^-8) over
+    bf16 rows, to f16 (2^-11) over FP8 rows, whose codes are f16 exactly.  There p * scale is held in units of the largest
+    one so far of its head and 64 channels, which lies above 2^12 of them: where f16 ends below 2^-14, a step is 2^-24
+    units, and a key adds at most half of it, 2^-37 of the largest p * scale, times its code (448 at most).  The units
+    end at 2^-100, so that half a step is never below 2^-125."""
+    n, HK, d = k.shape
+    half = 0.0 if act == "f32" or cache == "f32" else 2.0 ** -8 if cache == "bf16" else 2.0 ** -11
+    out, tol = attend(q, k, v, scale, torch.ones(1, n, dtype=torch.bool), sinks, DT[act], half)
+    if act == "bf16" and cache == "fp8":
+        G = q.shape[1] // HK
+        for h in range(q.shape[1]):
+            lg = (k[:, h // G] @ q[0, h]) * scale
+            top = max(float(lg.max()), float(sinks[h]) if sinks is not None else -float("inf"))
+            w = torch.exp(lg - top)
+            den = w.sum() + (torch.exp(sinks[h].double() - top) if sinks is not None else 0.0)
+            most = (w[:, None] * v_scales[:, h // G]).amax(0)              # [d/64]
+            unit = torch.clamp(2.0 ** -37 * most, min=2.0 ** -125) / den
+            tol[0, h] += n * 448 * unit.repeat_interleave(64)
+    return out, tol
+
+
+def scale_rows(cache, table_row, n, page):
+    """The scales of rows 0..n-1 of one sequence, [n][HK][d/64] float64."""
+    ids = table_row[:-(-n // page)].long().clamp(min=0)
+    s = cache.scales[ids.to(cache.scales.device)].cpu().double()
+    return s.transpose(1, 2).reshape(-1, s.shape[1], s.shape[3])[:n]
 
 
 @pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 200])
@@ -28,3 +59,34 @@ def test_prompt_with_a_window_that_hides_nothing(act, H, HK, d, window):
     assert (out[180:300] != 0).any() and (out[:180] == 0).all()
     p.window = 0
     assert torch.equal(out, run_prompt(p, q.cuda(), k.cuda(), v.cuda(), cq, ck, sinks, act))
+
+
+@pytest.mark.parametrize("act,cache", [("bf16", "bf16"), ("bf16", "fp8"), ("f32", "f32")])
+@pytest.mark.parametrize("window", [0, 20, 2 ** 31 - 1])
+@pytest.mark.parametrize("pages", [12, 200], ids=["whole", "split"])
+def test_decode_at_any_position(act, cache, window, pages):
+    """Positions at both ends of 64 bits: below 0 a row is 0, past the table it has the places that exist and is flagged."""
+    g, _ = gen(72), clean()
+    p = make(4, 2, 64, act, cache, page_size=8, window=window)
+    cap = 8 * pages
+    pos = [-2 ** 63, 50, -2 ** 63 + 7, 2 ** 63 - 1, -1, 2 ** 63 - 9, cap - 1, 2 ** 40, cap + 5]
+    t = table_of(g, [pages] * len(pos), pages)
+    kc, vc = fill_cache(g, p, pages * len(pos), cache)
+    q, sinks = normal(g, len(pos), 4, 64, dt=DT[act]).cuda(), normal(g, 4)
+    ws = torch.empty(K.gqa_workspace_size(p, K.OP_PAGED_DECODE, len(pos), len(pos), cap), dtype=torch.uint8, device="cuda")
+    for i, at in enumerate(pos):
+        out, tab = torch.full((1, 4, 64), float("nan"), dtype=DT[act], device="cuda"), t[i:i + 1].cuda()
+        K.paged_decode_attn(p, 1, q[i:i + 1], kc, vc, tab, torch.tensor([at]).cuda(), sinks.cuda(), out, ws)
+        assert clean() == (K.DEV_BAD_INDEX if at >= cap else 0)
+        lo, n = max(at - window + 1, 0) if window else 0, max(min(at + 1, cap), 0)
+        if n <= lo:
+            assert (out == 0).all()
+            continue
+        k, v = (paged_rows(c, t[i], n, 8)[lo:] for c in (kc, vc))
+        vs = scale_rows(vc, t[i], n, 8)[lo:] if cache == "fp8" else None
+        ref, tol = attend_paged(q[i:i + 1].cpu().double(), k, v, vs, p.scale, sinks, act, cache)
+        assert_within(out, ref, tol, str(at))
+    every = torch.full_like(q, float("nan"))
+    K.paged_decode_attn(p, len(pos), q, kc, vc, t.cuda(), torch.tensor(pos).cuda(), sinks.cuda(), every, ws)
+    assert clean() == K.DEV_BAD_INDEX and torch.isfinite(every.float()).all()
+    assert all((every[i] == 0).all() for i, at in enumerate(pos) if at < 0)
