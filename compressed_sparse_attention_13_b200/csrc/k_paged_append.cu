@@ -119,6 +119,12 @@ __device__ int find_sequence(const int32_t* cu, int n_seq, int64_t i, int lane) 
     return lo;
 }
 
+// Position of the token `i` behind a sequence's first one at `first` >= 0: the last
+// there is where the sum would overflow (no table reaches it either).
+__device__ __forceinline__ int64_t place_of(int64_t first, int64_t i) {
+    return first > INT64_MAX - i ? INT64_MAX : first + i;
+}
+
 // Position of packed row tok and its sequence; -1 for a row of no sequence or of
 // one that is left out.  Called by a whole warp.
 __device__ __forceinline__ int64_t position_of(const PagedAppendArgs& a, int64_t tok, int lane, int& s) {
@@ -128,7 +134,7 @@ __device__ __forceinline__ int64_t position_of(const PagedAppendArgs& a, int64_t
     }
     if (a.n_seq > 32) {
         s = find_sequence(a.cu_q, a.n_seq, tok, lane);
-        return s >= 0 && a.pos0[s] >= 0 ? a.pos0[s] + tok - a.cu_q[s] : -1;
+        return s >= 0 && a.pos0[s] >= 0 ? place_of(a.pos0[s], tok - a.cu_q[s]) : -1;
     }
     // up to 32 sequences: all loads at once
     const int32_t from = lane < a.n_seq ? a.cu_q[lane] : INT32_MAX, end = a.cu_q[a.n_seq];
@@ -137,7 +143,7 @@ __device__ __forceinline__ int64_t position_of(const PagedAppendArgs& a, int64_t
     s = le && tok < end ? 31 - __clz(int(le)) : -1;
     const int64_t p = __shfl_sync(0xffffffffu, first, max(s, 0));
     const int32_t at = __shfl_sync(0xffffffffu, from, max(s, 0));
-    return s >= 0 && p >= 0 ? p + tok - at : -1;
+    return s >= 0 && p >= 0 ? place_of(p, tok - at) : -1;
 }
 
 template <int ACT, int FMT>

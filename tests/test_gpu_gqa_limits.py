@@ -90,3 +90,25 @@ def test_decode_at_any_position(act, cache, window, pages):
     K.paged_decode_attn(p, len(pos), q, kc, vc, t.cuda(), torch.tensor(pos).cuda(), sinks.cuda(), every, ws)
     assert clean() == K.DEV_BAD_INDEX and torch.isfinite(every.float()).all()
     assert all((every[i] == 0).all() for i, at in enumerate(pos) if at < 0)
+
+
+@pytest.mark.parametrize("n_seq", [3, 40])
+def test_append_of_tokens_past_every_table(n_seq):
+    """Positions up to the last one of 64 bits: such tokens are flagged and not written, and their queries and keys come out
+    as those of a token, not as those of a sequence that is left out."""
+    g, _ = gen(73), clean()
+    p = make(2, 1, 64, page_size=4)
+    starts = [2 ** 63 - 2, 0, 2 ** 40] + [0] * (n_seq - 3)
+    lens = [5, 6, 2] + [1] * (n_seq - 3)
+    n = sum(lens)
+    cu = torch.tensor([sum(lens[:i]) for i in range(n_seq + 1)], dtype=torch.int32)
+    t = torch.arange(2 * n_seq, dtype=torch.int32).view(n_seq, 2)
+    kc, vc = K.empty_paged(p, 2 * n_seq)
+    kc.data.zero_(), vc.data.zero_()
+    q, k, v = (normal(g, n, h, 64, dt=torch.bfloat16).cuda() for h in (2, 1, 1))
+    qo, ko = torch.full_like(q, 5), torch.full_like(k, 5)
+    K.paged_append(p, n_seq, n, cu.cuda(), torch.tensor(starts).cuda(), q, k, v, None, qo, ko, kc, vc, t.cuda())
+    assert clean() == K.DEV_BAD_INDEX
+    assert torch.equal(qo, q) and torch.equal(ko, k)   # nothing is rotated
+    assert torch.equal(kc.data[2:4, 0].flatten(0, 1)[:6], k[5:11, 0]) and torch.equal(vc.data[2:4, 0].flatten(0, 1)[:6], v[5:11, 0])
+    assert not kc.data[[0, 1, 4, 5]].any() and not vc.data[[0, 1, 4, 5]].any()
