@@ -49,10 +49,15 @@ class PagedLayer:
 
     def prefill(self, lens, q, k, v, sinks, out):
         """The whole prompts of empty sequences: lens[s] tokens of sequence s (0: none), packed
-        in q [n][H][d], k, v [n][HK][d]; out [n][H][d].  The rotated queries and keys live until
-        the attention has read them."""
+        in q [n][H][d], k, v [n][HK][d]; out [n][H][d].  Rows from sum(lens) on are padding.  The
+        rotated queries and keys live until the attention has read them."""
         import torch
-        assert len(lens) == self.n_seq and all(not n or not self.lens[s] for s, n in enumerate(lens))
+        if len(lens) != self.n_seq or any(n < 0 for n in lens):
+            raise ValueError(f"lens must be {self.n_seq} lengths of at least 0, got {list(lens)}")
+        if any(n and self.lens[s] for s, n in enumerate(lens)):
+            raise ValueError("a prompt for a sequence that holds tokens: release it first")
+        if sum(lens) > q.shape[0]:
+            raise ValueError(f"prompts of {sum(lens)} tokens in {q.shape[0]} rows")
         for s, n in enumerate(lens):
             self.reserve(s, n)
         cu = [0]

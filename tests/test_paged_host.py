@@ -1,0 +1,37 @@
+"""The paged layer's own checks: what it refuses, and that a refused call leaves it as it was (no GPU)."""
+import pytest
+import torch
+
+import compressed_sparse_attention_13_b200 as K
+from compressed_sparse_attention_13_b200.paged import PagedLayer
+
+
+def layer(n_seq=3, n_pages=6, max_pages=4):
+    return PagedLayer(K.gqa_params(8, 2, 128, 0.1, page_size=4), n_seq=n_seq, n_pages=n_pages, max_pages=max_pages, device="cpu")
+
+
+def state(lay):
+    return list(lay.lens), [list(h) for h in lay._held], sorted(lay._free), lay.table.tolist(), lay.pos.tolist()
+
+
+@pytest.mark.parametrize("lens", [[5, 4, 2], [0, 0, 11], [11, 0, 0]])
+def test_a_prefill_of_more_tokens_than_rows_is_refused(lens):
+    lay = layer()
+    q, k, v = (torch.zeros(10, h, 128, dtype=torch.bfloat16) for h in (8, 2, 2))
+    before = state(lay)
+    with pytest.raises(ValueError, match="11 tokens in 10 rows"):
+        lay.prefill(lens, q, k, v, None, torch.zeros_like(q))
+    assert state(lay) == before
+
+
+@pytest.mark.parametrize("lens,match", [([1, 2], "3 lengths"), ([1, 2, 3, 0], "3 lengths"), ([4, -1, 2], "at least 0"),
+                                        ([0, 3, 0], "holds tokens")])
+def test_a_prefill_of_wrong_lengths_is_refused(lens, match):
+    lay = layer()
+    lay.reserve(1, 3)
+    lay.lens[1] = 3
+    q, k, v = (torch.zeros(10, h, 128, dtype=torch.bfloat16) for h in (8, 2, 2))
+    before = state(lay)
+    with pytest.raises(ValueError, match=match):
+        lay.prefill(lens, q, k, v, None, torch.zeros_like(q))
+    assert state(lay) == before
