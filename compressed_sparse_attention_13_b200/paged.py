@@ -76,10 +76,12 @@ class PagedLayer:
 
     def advance(self, active=None):
         """Host side of a decode step: room for one more token of each active sequence (all
-        that hold tokens, when not given), whose positions move on by one.  A sequence left
-        out is at position -1 in this step."""
+        that hold tokens, when not given; each named once), whose positions move on by one.  A
+        sequence left out is at position -1 in this step."""
         import torch
         active = [s for s, n in enumerate(self.lens) if n] if active is None else list(active)
+        if len(set(active)) != len(active) or any(not 0 <= s < self.n_seq for s in active):
+            raise ValueError(f"active must name sequences 0 to {self.n_seq - 1}, each once, got {active}")
         for s in active:  # all of them before any length moves: a full pool leaves the lengths as they were
             self.reserve(s, 1)
         for s in active:

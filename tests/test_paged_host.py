@@ -35,3 +35,18 @@ def test_a_prefill_of_wrong_lengths_is_refused(lens, match):
     with pytest.raises(ValueError, match=match):
         lay.prefill(lens, q, k, v, None, torch.zeros_like(q))
     assert state(lay) == before
+
+
+@pytest.mark.parametrize("active", [[1, 1], [0, 2, 0], [3], [-1], [2, -1]])
+def test_a_step_of_a_sequence_named_twice_or_of_none_is_refused(active):
+    """Named twice, a sequence would move on by two tokens with room for one, and only one of them would be written."""
+    lay = layer()
+    for s in range(3):
+        lay.reserve(s, 4)
+        lay.lens[s] = 4
+    before = state(lay)
+    with pytest.raises(ValueError, match="each once"):
+        lay.advance(active)
+    assert state(lay) == before
+    lay.advance([2, 0])
+    assert lay.lens == [5, 4, 5] and lay.pos.tolist() == [4, -1, 4]
