@@ -28,15 +28,30 @@ class PagedLayer:
         self.ws = torch.empty(gqa_workspace_size(p, OP_PAGED_DECODE, n_seq, n_seq, max_pages * p.page_size),
                               dtype=torch.uint8, device=device)
 
+    def _missing(self, s: int, n: int) -> int:
+        """Pages that sequence s lacks for n more tokens."""
+        return max(-(-(self.lens[s] + n) // self.p.page_size) - len(self._held[s]), 0)
+
+    def _check_room(self, wants):
+        """Raise, before any page is taken, unless the pool and the table hold n more tokens of each
+        sequence s, for all (s, n)."""
+        free = len(self._free)
+        for s, n in wants:
+            need = self._missing(s, n)
+            free -= need
+            if free < 0 or len(self._held[s]) + need > self.table.shape[1]:
+                raise RuntimeError(f"sequence {s}: no room for {n} more tokens")
+
     def reserve(self, s: int, n: int):
         """Pages for the next n tokens of sequence s (raises when the pool or the table is full)."""
-        import torch
-        need = -(-(self.lens[s] + n) // self.p.page_size) - len(self._held[s])
-        if need <= 0:
+        self._check_room([(s, n)])
+        self._take(s, n)
+
+    def _take(self, s: int, n: int):
+        need, first = self._missing(s, n), len(self._held[s])
+        if need == 0:
             return
-        if need > len(self._free) or len(self._held[s]) + need > self.table.shape[1]:
-            raise RuntimeError(f"sequence {s}: no room for {n} more tokens")
-        first = len(self._held[s])
+        import torch
         self._held[s] += [self._free.pop() for _ in range(need)]
         self.table[s, first:first + need] = torch.tensor(self._held[s][first:], dtype=torch.int32)
 
@@ -58,8 +73,9 @@ class PagedLayer:
             raise ValueError("a prompt for a sequence that holds tokens: release it first")
         if sum(lens) > q.shape[0]:
             raise ValueError(f"prompts of {sum(lens)} tokens in {q.shape[0]} rows")
+        self._check_room(enumerate(lens))
         for s, n in enumerate(lens):
-            self.reserve(s, n)
+            self._take(s, n)
         cu = [0]
         for n in lens:
             cu.append(cu[-1] + n)
@@ -82,8 +98,9 @@ class PagedLayer:
         active = [s for s, n in enumerate(self.lens) if n] if active is None else list(active)
         if len(set(active)) != len(active) or any(not 0 <= s < self.n_seq for s in active):
             raise ValueError(f"active must name sequences 0 to {self.n_seq - 1}, each once, got {active}")
-        for s in active:  # all of them before any length moves: a full pool leaves the lengths as they were
-            self.reserve(s, 1)
+        self._check_room((s, 1) for s in active)  # a full pool leaves everything as it was
+        for s in active:
+            self._take(s, 1)
         for s in active:
             self.lens[s] += 1
         pos = [-1] * self.n_seq

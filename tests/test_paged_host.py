@@ -50,3 +50,24 @@ def test_a_step_of_a_sequence_named_twice_or_of_none_is_refused(active):
     assert state(lay) == before
     lay.advance([2, 0])
     assert lay.lens == [5, 4, 5] and lay.pos.tolist() == [4, -1, 4]
+
+
+def test_prompts_that_find_no_room_take_no_pages():
+    """The pool holds the first two prompts and not the third: none of its pages stays with an empty sequence."""
+    lay = layer()
+    q, k, v = (torch.zeros(30, h, 128, dtype=torch.bfloat16) for h in (8, 2, 2))
+    before = state(lay)
+    for lens in ([8, 8, 9], [8, 0, 17]):   # 2 + 2 + 3 of 6 pages; 5 pages of a table of 4
+        with pytest.raises(RuntimeError, match="sequence 2: no room"):
+            lay.prefill(lens, q, k, v, None, torch.zeros_like(q))
+        assert state(lay) == before
+    for s, n in ((0, 8), (1, 8), (2, 8)):
+        lay.reserve(s, n)
+        lay.lens[s] = n
+    lay.release(2)
+    lay.reserve(2, 3)
+    lay.lens[2] = 3
+    before = state(lay)
+    with pytest.raises(RuntimeError, match="sequence 1: no room"):
+        lay.advance()      # one page is left for the two that need one
+    assert state(lay) == before
