@@ -101,8 +101,6 @@ __device__ __forceinline__ uint2 codes_of(const Chunk& x, float s) {
     return make_uint2(w[0], w[1]);
 }
 
-}  // namespace
-
 // The sequence of packed row i: the last s with cu[s] <= i, or -1 for a row
 // behind the last sequence.  One warp, 32 probes a step.
 __device__ int find_sequence(const int32_t* cu, int n_seq, int64_t i, int lane) {
@@ -145,6 +143,8 @@ __device__ __forceinline__ int64_t position_of(const PagedAppendArgs& a, int64_t
     const int32_t at = __shfl_sync(0xffffffffu, from, max(s, 0));
     return s >= 0 && p >= 0 ? place_of(p, tok - at) : -1;
 }
+
+}  // namespace
 
 template <int ACT, int FMT>
 __global__ void __launch_bounds__(kAppendThreads, ACT == CSA_F32 ? 5 : 7)

@@ -154,8 +154,4 @@ cudaError_t launch_prompt_simt(const PromptArgs& a, cudaStream_t s);
 bool prompt_tc_supported(const PromptArgs& a);
 cudaError_t launch_prompt_tc(const PromptArgs& a, cudaStream_t s);
 
-// The sequence of packed row i: the last s with cu[s] <= i, or -1 for a row
-// behind the last sequence.  Called by a whole warp.
-__device__ int find_sequence(const int32_t* cu, int n_seq, int64_t i, int lane);
-
 }  // namespace csa
