@@ -21,15 +21,18 @@
 //
 // 32 sequences of up to 11,073 tokens, 32 heads over 8 (682 MB): 110 us, 6.2 TB/s;
 // four of up to 131,072, 64 heads over 8 (1752 MB): 267 us, 6.6 TB/s; 16 of up to
-// 32,768 in FP8, 32 heads over 8 (1006 MB): 163 us, 6.2 TB/s.
+// 32,768 in FP8, 32 heads over 8 (1006 MB): 163 to 183 us on different boards, 5.5 to
+// 6.2 TB/s.
 //
 // FP8 entries (E4M3 codes, fp32 scale per 64 channels) are converted to f16
 // exactly, one instruction per pair, and the MMAs run in f16: the query is
 // scaled by a power of two per head (exact within 2^26 of the head's largest
 // element), the key scales multiply S per 64 channels, and P takes the value
-// scales.  So that p * scale fits f16 whatever the scales, it is kept
-// relative to a power of two per (head, 64 channels) that follows its running
-// maximum, and O is in those units.
+// scales.  So that p * scale fits f16 whatever the scales, it is kept in units
+// per (head, 64 channels) that follow its running maximum, and O is in those
+// units: a power of two when they are set, times what the row's maximum has grown
+// since.  They lie between 2^-100 and 2^100, S is formed in fp32 from the codes'
+// products: entries up to 2^100 in magnitude are safe.
 #include "paged_split.cuh"
 
 namespace csa {
@@ -192,7 +195,7 @@ __global__ void __launch_bounds__(32 * kNW, Dec<D, FP8, NT>::kCtas)
         }
         float o[NT][D / 16][4];
         float m[NT][2], l[NT][2];
-        float f[NT][FP8 ? C::kGroups : 1][2];  // FP8: the power of two that P is multiplied by
+        float f[NT][FP8 ? C::kGroups : 1][2];  // FP8: what P is multiplied by
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll

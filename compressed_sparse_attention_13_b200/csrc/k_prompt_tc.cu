@@ -40,7 +40,9 @@
 // same on one long prompt, 11% longer on a packed batch of short ones), and a
 // persistent CTA that loads and multiplies the next tile under the end of this
 // one (1% shorter on a packed batch, 5% longer on one prompt).  16,384 tokens,
-// 32 heads over 8: 2.03 ms, 1.08 PFLOP/s, at the board's power limit.
+// 32 heads over 8: 2.03 to 2.12 ms on different boards in a loop of calls, 1.04 to
+// 1.08 PFLOP/s, at the board's power limit (a single call from cold caches 1.82 ms).
+// The d = 128 kernel spills 20 bytes at the 168 registers that 384 threads leave.
 //
 // Waits are bounded (sm100.cuh).  Compiled as a whole program: setmaxnreg
 // moves registers from the other warps to the softmax.

@@ -27,6 +27,8 @@ constexpr int kMinSteps = 2;           // a block's share is not cut finer than 
 // 12 / 39 / 30 sequences, most of them short, bf16 at d = 128 / 256 / 64 (us):
 //   cost 0: 30 / 43 / 58,  2: 18 / 26 / 28,  3: 17 / 27 / 25,  6: 17 / 32 / 23
 // (one long row of 32 heads over 8, 1,001 tokens: 10.9 / 11.5 / 11.3 / 11.3).
+// Measured with the tensor-core kernel's steps of 64 tokens; the CUDA-core kernel's
+// steps of 32 use it too.
 constexpr int kUnitCost = 3;
 constexpr uint32_t kNoRow = 0xFFFFFFFFu;
 

@@ -437,6 +437,9 @@ int attn_merge(const csa_params* p, int32_t batch, int32_t n_parts, const float*
  * Packed batches: the tokens of sequence s are rows cu[s] .. cu[s+1] - 1
  * (cu: int32 [n_seq + 1], device, not decreasing, cu[0] = 0).  Rows from
  * cu[n_seq] on (padding) are neither read for another row nor written.
+ * Range: sums of e^(l_i-M) v_i are held in fp32, with a maximum up to 8 log2
+ * units below M while a row is walked: with n visible tokens, values up to
+ * 2^120 / n in magnitude are safe, and keys and values up to 2^100 in FP8 pages.
  * ======================================================================== */
 
 /* Parameters of the grouped-head calls.  H / HK <= 128; d 64, 128, 192 or
@@ -465,7 +468,8 @@ typedef struct csa_gqa_params {
 /* Bytes of workspace paged_decode_attn (n_seq = batch) or prompt_attn needs;
  * 0 on bad arguments.  A workspace needs no initial contents; calls that may
  * overlap need one each.  n_tokens: query tokens; n_ctx: rows that a sequence
- * can hold (max_pages * page_size); both may be upper bounds. */
+ * can hold (max_pages * page_size); both may be upper bounds.  (prompt_attn's
+ * is a fixed 256 bytes, reserved: its kernels use none of them so far.) */
 size_t csa_gqa_workspace_size(const csa_gqa_params* p, int32_t op, int32_t n_seq, int64_t n_tokens,
                               int64_t n_ctx);
 
@@ -478,7 +482,8 @@ size_t csa_gqa_workspace_size(const csa_gqa_params* p, int32_t op, int32_t n_seq
  *   a' = a cos(t f_j) - b sin(t f_j),  b' = b cos(t f_j) + a sin(t f_j)
  * in fp32, the angle reduced in fp64; dims from R on are copied.  Every result
  * is rounded once: k' to act_fmt in k_out and from the same fp32 value to
- * cache_fmt in the cache (FP8_S64 by the rule of csa_quantize).
+ * cache_fmt in the cache (FP8_S64 by the rule of csa_quantize; a group whose
+ * amax / 448 underflows to 0 is stored as zeros with the scale 1).
  *   q:         [n_tokens][H][d], token stride q_ld; NULL: no queries
  *   k, v:      [n_tokens][HK][d], token strides k_ld, v_ld
  *   cu_q:      int32 [n_seq + 1], or NULL: one token per sequence (n_tokens = n_seq)
@@ -508,7 +513,8 @@ int paged_append(const csa_gqa_params* p, int32_t n_seq, int64_t n_tokens, const
  * a fixed order; with CSA_FLAG_BATCH_INVARIANT the parts of a row depend on
  * its own length only.
  *   q:         [batch][H][d] in act_fmt, row stride q_ld
- *   q_pos:     int64 [batch]
+ *   q_pos:     int64 [batch], any value: of a row whose t is past the table
+ *              (CSA_DEV_BAD_INDEX) the visible tokens that have a place count
  *   sinks:     float [H] or NULL
  *   out:       [batch][H][d] in act_fmt
  *   workspace: >= csa_gqa_workspace_size(p, CSA_OP_PAGED_DECODE, batch, batch,
@@ -529,9 +535,9 @@ int paged_decode_attn(const csa_gqa_params* p, int32_t batch, const void* q, int
  * position t = i + len_k - len_q and sees the keys j <= t (and j > t-W), by
  * the softmax of paged_decode_attn.  For whole prompts cu_k is cu_q; a later
  * chunk of a prompt has more keys than queries.  A query without a visible
- * key (t < 0) gives 0.  Values and keys that a query does not see, infinities
- * and NaN among them, do not reach its output.  p->page_size and p->cache_fmt
- * are not used.
+ * key (t < 0) gives 0.  W may be anything up to INT32_MAX.  Values and keys
+ * that a query does not see, infinities and NaN among them, do not reach its
+ * output.  p->page_size and p->cache_fmt are not used.
  *   q:         [n_q][H][d] in act_fmt, token stride q_ld
  *   k, v:      [n_k][HK][d] in act_fmt, token strides k_ld, v_ld
  *   cu_q, cu_k: int32 [n_seq + 1]

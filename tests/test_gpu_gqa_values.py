@@ -222,3 +222,39 @@ def test_prompt_of_logits_that_grow_along_the_keys(act, H, HK, d, kind):
     m = int(cq[-1])
     assert clean() == 0
     assert_within(out[:m], ref[:m], tol[:m], kind)
+
+
+@pytest.mark.parametrize("act,d", [("bf16", 64), ("bf16", 128), ("f32", 64), ("f32", 192), ("f32", 256)])
+@pytest.mark.parametrize("one", [False, True], ids=["packed", "single"])
+def test_append_quantises_as_csa_quantize_does(act, d, one):
+    """Rows that are not rotated: the same codes and scales bit for bit, for values of any size and for those that are no
+    numbers.  One difference is documented: a group so small that its scale is 0 in fp32 is stored as zeros with scale 1."""
+    g, _ = gen(87), clean()
+    n, HK, page = 600, 3, 16
+    p = make(3, HK, d, act, "fp8", page_size=page)
+    x = normal(g, 2, n, HK, d) * torch.exp2(torch.randint(-30, 31, (2, n, HK, 1), generator=g).float())
+    x[:, 1] = 0.0
+    x[:, 2] *= 1e-38                                     # scales that leave the normal range
+    x[:, 3] = torch.exp2(torch.randint(-149, -120, (2, HK, d), generator=g).double()).float()
+    x[:, 4] = 3e38
+    x[:, 5] = torch.exp2(torch.randint(-9, 1, (2, HK, d), generator=g).float()) * (1 + torch.randint(0, 8, (2, HK, d), generator=g) / 16)
+    for i, bad in ((6, float("nan")), (7, float("inf")), (8, float("-inf"))):
+        x[:, i, :, i::64] = bad
+    x = x.to(DT[act]).cuda()
+    pages = -(-n // page) if not one else n
+    kc, vc = K.empty_paged(p, pages)
+    pos, cu = (torch.zeros(n, dtype=torch.int64), None) if one else (torch.zeros(1, dtype=torch.int64), torch.tensor([0, n], dtype=torch.int32).cuda())
+    t = torch.arange(pages, dtype=torch.int32).view(n, 1) if one else torch.arange(pages, dtype=torch.int32)[None]
+    K.paged_append(p, len(pos), n, cu, pos.cuda(), None, x[0], x[1], None, None, None, kc, vc, t.cuda())
+    i = torch.arange(n)
+    at = (i, slice(None), 0 * i) if one else (i // page, slice(None), i % page)
+    for c, y in ((kc, x[0]), (vc, x[1])):
+        want = K.empty_stored(K.FP8_S64, n * HK, d)
+        K.csa_quantize(y.float().reshape(-1, d), want)
+        codes, scales = want.data.view(n, HK, -1, 64), want.scales.view(n, HK, -1)
+        none = scales == 0        # amax / 448 underflows: here the group counts as one of zeros
+        scales = torch.where(none, 1.0, scales)
+        assert torch.equal(c.scales[at].view(torch.int32), scales.view(torch.int32))
+        got = c.data[at].unflatten(-1, (-1, 64))
+        assert torch.equal(got[~none], codes[~none]) and not (got[none] & 0x7F).any()
+    assert clean() == 0
